@@ -1,0 +1,429 @@
+"""Cases, plain forms and exact values of the serving operators: the head
+normalisation and rotation of projected rows, the paged key-value cache
+(written, quantised or not, and read back), and the attention of a few new
+tokens over it.
+
+``own`` chooses what :func:`run` does: the plain forms in elementary torch
+operations (32 bits, rounded once at the end), or the library's calls.
+
+Sizes: the layer geometry is the one of the pre-fill workloads (32 query and 8
+KV heads of 128, or 8 / 2 and 4 / 2 heads of 64 for small layers), caches from
+one token to 1,048,576.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+ROPE_BASE = 500000.0
+E4M3 = torch.float8_e4m3fn
+
+
+# ------------------------------------------------------------------------ cases
+def listed():
+    layer = dict(Hq=32, Hkv=8, d=128)
+    return [
+        # one generated token of one request: the smallest call, latency only
+        dict(name="rope_one_token", op="rope", B=1, N=1, norm=True, rot=128, inter=False, far=100000, **layer),
+        # drafted trees of a small batch; a small layer, part of each head rotated, neighbouring pairs, no norm
+        dict(name="rope_tree_d64", op="rope", B=7, N=29, Hq=8, Hkv=2, d=64, norm=False, rot=32, inter=True, far=1000000),
+        # the prompt of the 128K layer
+        dict(name="rope_prompt_128k", op="rope", B=1, N=131072, norm=True, rot=128, inter=False, far=0, **layer),
+        # one generated token of each of 48 requests into an 8-bit cache of short pages
+        dict(name="write_tokens_e4m3", op="write", B=48, N=1, ctx=30000, page=16, e4m3=True, ragged=True, **layer),
+        # a prompt's keys and values into an 8-bit cache
+        dict(name="write_prompt_e4m3", op="write", B=1, N=131072, ctx=0, page=64, e4m3=True, ragged=False, **layer),
+        # a ragged batch's prefixes out of a 16-bit cache, an odd number of rows
+        dict(name="read_ragged_bf16_d64", op="read", B=5, N=2500, Hq=8, Hkv=2, d=64, page=128, e4m3=False, ragged=True),
+        # a long prefix out of the 8-bit cache, for the pre-fill of what follows it
+        dict(name="read_prompt_e4m3", op="read", B=1, N=131072, page=64, e4m3=True, ragged=False, **layer),
+        # one token of one request after a 4K prompt
+        dict(name="attn_one_token_4k", op="attn", B=1, T=1, ctx=4095, page=64, e4m3=False, ragged=False, tree=False, **layer),
+        # small trees of a small batch, a small layer, 8-bit cache
+        dict(name="attn_tree13_d64", op="attn", B=4, T=13, Hq=4, Hkv=2, d=64, ctx=9000, page=32, e4m3=True, ragged=True,
+             tree=True),
+        # a serving batch, one token each, lengths from a few tokens to 16K
+        dict(name="attn_batch32_16k", op="attn", B=32, T=1, ctx=16384, page=16, e4m3=True, ragged=True, tree=False, **layer),
+        # a wide drafted tree after a 128K prompt
+        dict(name="attn_tree64_128k", op="attn", B=1, T=64, ctx=131000, page=128, e4m3=False, ragged=False, tree=True, **layer),
+        # one token after a 1M-token prompt, 8-bit cache
+        dict(name="attn_one_token_1m", op="attn", B=1, T=1, ctx=1048570, page=64, e4m3=True, ragged=False, tree=False, **layer),
+    ]
+
+
+def draw(rng):
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    c = dict(rng.choice([dict(Hq=32, Hkv=8, d=128)] * 3 + [dict(Hq=8, Hkv=2, d=64), dict(Hq=4, Hkv=2, d=64), dict(Hq=8, Hkv=8, d=128),
+                                                           dict(Hq=6, Hkv=2, d=128)]))
+    c["op"] = rng.choice(["rope", "write", "read", "attn", "attn", "attn"])
+    if c["op"] == "rope":
+        c["B"] = log(1, 64)
+        c["N"] = log(1, 131072 // c["B"])
+        c["rot"] = rng.choice([c["d"], c["d"], c["d"] // 2, 32])
+        return dict(c, norm=rng.random() < 0.6, inter=rng.random() < 0.4, far=rng.choice([0, 1000, 900000]))
+    c["page"] = rng.choice([16, 32, 64, 128])
+    c["e4m3"] = rng.random() < 0.6
+    c["ragged"] = rng.random() < 0.6
+    c["B"] = log(1, 64)
+    if c["op"] == "attn":
+        c["T"] = rng.choice([1, 1, 1, 2, 5, rng.randint(3, 24), rng.randint(24, 64)])
+        most = min(131072, 131072 * 64 * 4 // (c["T"] * (c["Hq"] // c["Hkv"])))
+        c["B"] = min(c["B"], 32)
+        return dict(c, ctx=log(1, most // c["B"]), tree=c["T"] > 1 and rng.random() < 0.8)
+    c["N"] = log(1, 131072 // c["B"])
+    if c["op"] == "write":
+        c["ctx"] = rng.choice([0, log(1, 131072 // c["B"])])
+    return c
+
+
+# ----------------------------------------------------------------------- inputs
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(int(seed))
+
+
+def _randint(g, lo, hi, n):
+    """n integers in [lo, hi]."""
+    return torch.randint(lo, hi + 1, (n,), generator=g, device=DEV, dtype=torch.int32)
+
+
+def _keys_values(g, B, H, N, d):
+    """Keys with uneven channels and a first token that every query likes;
+    values of uneven size, the first token's small.  One unit vector per KV head
+    carries that liking; it is returned for the queries."""
+    gain = torch.exp(0.5 * torch.randn(1, H, 1, d, generator=g, device=DEV))
+    u = torch.randn(1, H, 1, d, generator=g, device=DEV)
+    u = u / u.norm(dim=-1, keepdim=True)
+    k = torch.randn(B, H, N, d, generator=g, device=DEV) * gain
+    k[:, :, :1] += 8.0 * u
+    k = k.to(torch.bfloat16)
+    v = torch.randn(B, H, N, d, generator=g, device=DEV) * torch.exp(0.3 * torch.randn(B, H, N, 1, generator=g, device=DEV))
+    v[:, :, :1] *= 0.1
+    return k, v.to(torch.bfloat16), u
+
+
+def _pages(g, B, rows, page):
+    """A table that scatters the sequences' pages over a pool with a few spare ones."""
+    per = -(-rows // page)
+    n = B * per + 3
+    perm = torch.randperm(n, generator=g, device=DEV)[: B * per]
+    return perm.view(B, per).to(torch.int32), n
+
+
+def _pool_rows(pages, at, page):
+    """(page id, row within it) of positions `at` [B, N]."""
+    return torch.gather(pages.long(), 1, at // page), at % page
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    s = dict(case, plan=None)
+    B, Hq, Hkv, d = case["B"], case["Hq"], case["Hkv"], case["d"]
+    if case["op"] == "rope":
+        N = case["N"]
+        s["qkv"] = torch.randn(B, N, (Hq + 2 * Hkv) * d, generator=g, device=DEV, dtype=torch.bfloat16)
+        s["pos"] = (torch.arange(N, device=DEV, dtype=torch.int32)[None] + _randint(g, 0, case["far"], B)[:, None]).contiguous()
+        s["inv_freq"] = ROPE_BASE ** (-torch.arange(0, case["rot"], 2, device=DEV, dtype=torch.float64) / case["rot"])
+        s["qw"] = s["kw"] = None
+        if case["norm"]:
+            s["qw"], s["kw"] = ((1 + 0.2 * torch.randn(d, generator=g, device=DEV)).to(torch.bfloat16) for _ in "qk")
+        return s
+    page = case["page"]
+    if case["op"] == "write":
+        N = case["N"]
+        s["k"], s["v"], _ = _keys_values(g, B, Hkv, N, d)
+        s["pages"], n = _pages(g, B, case["ctx"] + N, page)
+        s["start"] = _randint(g, 0, case["ctx"], B) if case["ragged"] else torch.full((B,), case["ctx"], device=DEV, dtype=torch.int32)
+        s["count"] = _randint(g, max(1, N // 2), N, B) if case["ragged"] else torch.full((B,), N, device=DEV, dtype=torch.int32)
+        shape = (n, Hkv, page, d)
+        s["kp"], s["vp"] = (torch.zeros(shape, device=DEV, dtype=torch.uint8 if case["e4m3"] else torch.bfloat16) for _ in "kv")
+        s["ke"], s["ve"] = (torch.zeros(shape[:3], device=DEV, dtype=torch.uint8) if case["e4m3"] else None for _ in "kv")
+        if case["e4m3"]:
+            s["kp"], s["vp"] = s["kp"].view(E4M3), s["vp"].view(E4M3)
+        return s
+    rows = case["N"] if case["op"] == "read" else case["ctx"] + case["T"]
+    k, v, u = _keys_values(g, B, Hkv, rows, d)
+    s["pages"], n = _pages(g, B, rows, page)
+    at = torch.arange(rows, device=DEV)[None].expand(B, rows)
+    where = _pool_rows(s["pages"], at, page)
+    s["kp"], s["ke"] = _fill_pool(k, case, n, where)
+    s["vp"], s["ve"] = _fill_pool(v, case, n, where)
+    if case["op"] == "read":
+        s["lens"] = _randint(g, 0, rows, B) if case["ragged"] else torch.full((B,), rows, device=DEV, dtype=torch.int32)
+        return s
+    T = case["T"]
+    q = torch.randn(B, Hq, T, d, generator=g, device=DEV) + 8.0 * u.repeat_interleave(Hq // Hkv, dim=1)
+    s["q"] = q.to(torch.bfloat16)
+    s["ctx_lens"] = _randint(g, 0, case["ctx"], B) if case["ragged"] else torch.full((B,), case["ctx"], device=DEV, dtype=torch.int32)
+    s["mask"] = None
+    if case["tree"]:  # token t hangs under an earlier one and sees its ancestors and itself; bit u of word t: t sees u
+        parent = [int(x) for x in (torch.rand(T, generator=torch.Generator().manual_seed(int(seed))) * torch.arange(T)).floor()]
+        words = [1]
+        for t in range(1, T):
+            words.append(words[parent[t]] | 1 << t)
+        words = [w - (1 << 64) if w >> 63 else w for w in words]
+        s["mask"] = torch.tensor([words] * B, dtype=torch.int64, device=DEV)
+    return s
+
+
+def _fill_pool(x, case, n, where):
+    """A pool [n, Hkv, page, d] holding the rows of x at the given places."""
+    B, H, N, d = x.shape
+    pool = torch.zeros(n, H, case["page"], d, device=DEV, dtype=torch.uint8 if case["e4m3"] else torch.bfloat16)
+    if not case["e4m3"]:
+        pool[where[0], :, where[1]] = x.transpose(1, 2)
+        return pool, None
+    exps = torch.zeros(n, H, case["page"], device=DEV, dtype=torch.uint8)
+    q, e = _quantise(x)
+    pool[where[0], :, where[1]] = q.view(torch.uint8).transpose(1, 2)
+    exps[where[0], :, where[1]] = e.transpose(1, 2)
+    return pool.view(E4M3), exps
+
+
+# ------------------------------------------------------------------ plain forms
+def _power(e):
+    """2^(e - 127) in 32 bits for a stored exponent e >= 1."""
+    return (e.to(torch.int32) << 23).view(torch.float32)
+
+
+def _quantise(x):
+    """Rows as e4m3 values times a power of two each: the smallest 2^e, e >= -80,
+    with max |x| <= 448 * 2^e (e = 0 for a row of zeros); stored as e + 127."""
+    x = x.float()
+    m, ex = torch.frexp(x.abs().amax(-1))
+    e = torch.where(m == 0, torch.zeros_like(ex), (ex - 9 + (m > 0.875)).clamp(min=-80))
+    return (x * _power(127 - e)[..., None]).to(E4M3), (e + 127).to(torch.uint8)
+
+
+def _dequantised(pool, exps):
+    return pool.float() if exps is None else pool.float() * _power(exps)[..., None]
+
+
+def _cache_rows(pool, exps, pages):
+    """The cache's rows in order, in 32 bits: [B, Hkv, pages * page, d]."""
+    ids = pages.long()
+    raw = (pool if exps is None else pool.view(torch.uint8))[ids]  # [B, P, Hkv, page, d]
+    x = raw.float() if exps is None else raw.view(E4M3).float() * _power(exps[ids])[..., None]
+    return x.transpose(1, 2).flatten(2, 3)
+
+
+def _plain_rope(s):
+    B, N, Hq, Hkv, d, rot = s["B"], s["N"], s["Hq"], s["Hkv"], s["d"], s["rot"]
+    x = s["qkv"].view(B, N, Hq + 2 * Hkv, d).transpose(1, 2)
+    q, k, v = x.split([Hq, Hkv, Hkv], dim=1)
+    angle = (s["pos"].double()[..., None] * s["inv_freq"])[:, None]
+    cos, sin = angle.cos().float(), angle.sin().float()
+
+    def turned(x, w):
+        x = x.float()
+        if w is not None:
+            x = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6) * w.float()
+        r = x[..., :rot]
+        a, b = (r[..., 0::2], r[..., 1::2]) if s["inter"] else (r[..., : rot // 2], r[..., rot // 2 :])
+        a, b = a * cos - b * sin, b * cos + a * sin
+        r = torch.stack([a, b], -1).flatten(-2) if s["inter"] else torch.cat([a, b], -1)
+        return torch.cat([r, x[..., rot:]], -1).to(torch.bfloat16)
+
+    return turned(q, s["qw"]), turned(k, s["kw"]), v.contiguous()
+
+
+def _plain_write(s):
+    N = s["N"]
+    n = torch.arange(N, device=DEV)[None]
+    at = s["start"].long()[:, None] + n
+    live = n < s["count"][:, None]
+    pid, row = _pool_rows(s["pages"], torch.where(live, at, 0), s["page"])
+    pid, row = pid[live], row[live]
+
+    def put(x, pool, exps):
+        x = x.transpose(1, 2)[live]  # [rows, Hkv, d]
+        if exps is None:
+            pool[pid, :, row] = x
+        else:
+            q, e = _quantise(x)
+            pool.view(torch.uint8)[pid, :, row] = q.view(torch.uint8)
+            exps[pid, :, row] = e
+
+    put(s["k"], s["kp"], s["ke"])
+    put(s["v"], s["vp"], s["ve"])
+    return s["kp"], s["vp"], s["ke"], s["ve"]
+
+
+def _plain_read(s):
+    live = torch.arange(s["N"], device=DEV)[None] < s["lens"][:, None]
+
+    def rows(pool, exps):
+        x = _cache_rows(pool, exps, s["pages"])[:, :, : s["N"]]
+        return torch.where(live[:, None, :, None], x, 0.0).to(torch.bfloat16)
+
+    return rows(s["kp"], s["ke"]), rows(s["vp"], s["ve"])
+
+
+def _sees(s, L):
+    """[B, T, L]: whether drafted token t sees the key at position j."""
+    T = s["T"]
+    j = torch.arange(L, device=DEV)
+    u = j[None] - s["ctx_lens"].long()[:, None]  # drafted index of position j
+    t = torch.arange(T, device=DEV)
+    if s["mask"] is None:
+        among = u[:, None] <= t[None, :, None]
+    else:
+        among = (s["mask"][:, :, None] >> u.clamp(0, 63)[:, None]) & 1 == 1
+    return ((u < 0)[:, None] | among) & (u < T)[:, None]
+
+
+def _plain_attn(s):
+    B, T, Hq, Hkv, d = s["B"], s["T"], s["Hq"], s["Hkv"], s["d"]
+    g = Hq // Hkv
+    k = _cache_rows(s["kp"], s["ke"], s["pages"])
+    L = k.shape[2]
+    p = s["q"].float().view(B, Hkv, g * T, d) @ k.transpose(2, 3) * (1.0 / math.sqrt(d))
+    del k
+    p = p.view(B, Hkv, g, T, L).masked_fill_(~_sees(s, L)[:, None, None], -math.inf)
+    top = p.amax(-1, keepdim=True)
+    p = p.sub_(top).exp_()
+    total = p.sum(-1, keepdim=True)
+    o = p.view(B, Hkv, g * T, L) @ _cache_rows(s["vp"], s["ve"], s["pages"])
+    o = o.view(B, Hkv, g, T, d) / total
+    return o.view(B, Hq, T, d).to(torch.bfloat16), (top + total.log()).view(B, Hq, T)
+
+
+# ------------------------------------------------------------ the library's calls
+def _plan(s):
+    """What a program makes once and keeps: the cache's handle and a workspace."""
+    from dynamic_sparse_attention_minf_b200 import minf
+
+    if s["plan"] is None:
+        cache = None if s["op"] == "rope" else minf.KVCache(s["kp"], s["vp"], s["ke"], s["ve"])
+        ws = minf.tree_attn_workspace(s["B"], s["Hq"], s["Hkv"], s["T"], s["d"]) if s["op"] == "attn" else minf.status_workspace()
+        s["plan"] = minf, cache, ws
+    return s["plan"]
+
+
+def _own_run(s):
+    minf, cache, ws = _plan(s)
+    if s["op"] == "rope":
+        return minf.minf_qkv_norm_rope(s["qkv"], s["Hq"], s["Hkv"], pos=s["pos"], inv_freq=s["inv_freq"], q_weight=s["qw"],
+                                       k_weight=s["kw"], eps=1e-6, interleaved=s["inter"], ws=ws)
+    if s["op"] == "write":
+        minf.minf_kv_write(s["k"], s["v"], cache, s["pages"], s["start"], count=s["count"], ws=ws)
+        return s["kp"], s["vp"], s["ke"], s["ve"]
+    if s["op"] == "read":
+        return minf.minf_kv_read(cache, s["pages"], s["lens"], s["N"], ws=ws)
+    return minf.minf_tree_attn(s["q"], cache, s["pages"], s["ctx_lens"], tree_mask=s["mask"], ws=ws)
+
+
+def run(state):
+    if own:
+        return _own_run(state)
+    return {"rope": _plain_rope, "write": _plain_write, "read": _plain_read, "attn": _plain_attn}[state["op"]](state)
+
+
+# ------------------------------------------------------------------------- work
+def work(case):
+    B, Hq, Hkv, d = case["B"], case["Hq"], case["Hkv"], case["d"]
+    if case["op"] == "rope":
+        rows = B * case["N"]
+        return {"bytes": 2 * rows * (Hq + 2 * Hkv) * d * 2 + 4 * rows, "flops": rows * (Hq + Hkv) * d * 7}
+    kv_row = 2 * Hkv * (d + 1 if case["e4m3"] else 2 * d)  # one token's keys and values in the cache
+    mean = 0.5 if case["ragged"] else 1.0
+    if case["op"] == "write":
+        rows = B * (case["N"] * (0.75 if case["ragged"] else 1.0))
+        return {"bytes": rows * (kv_row + 2 * Hkv * d * 2), "flops": rows * 2 * Hkv * d * 2}
+    if case["op"] == "read":
+        rows = B * case["N"] * mean
+        return {"bytes": rows * kv_row + B * case["N"] * 2 * Hkv * d * 2, "flops": rows * 2 * Hkv * d}
+    keys = B * (case["ctx"] * mean + case["T"])
+    return {"bytes": keys * kv_row + B * Hq * case["T"] * (4 * d + 4), "flops": 4 * keys * Hq * case["T"] * d}
+
+
+# ------------------------------------------------------------------ exact values
+def _scale64(e):
+    return torch.exp2(e.double() - 127.0)[..., None]
+
+
+def _seq64(pool, exps, ids, h, n):
+    """Rows 0 .. n-1 of one sequence's KV head h, in 64 bits."""
+    x = pool[:, h].reshape(pool.shape[0], -1).view(torch.uint8 if exps is not None else pool.dtype)[ids.long()]
+    x = (x.view(E4M3) if exps is not None else x).double().reshape(-1, pool.shape[3])[:n]
+    return x if exps is None else x * _scale64(exps[:, h][ids.long()].reshape(-1)[:n])
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    B, Hq, Hkv, d = case["B"], case["Hq"], case["Hkv"], case["d"]
+    if case["op"] == "rope":
+        N, rot = case["N"], case["rot"]
+        out = torch.empty(B, Hq + 2 * Hkv, N, d, device=DEV, dtype=torch.float64)
+        half = torch.arange(rot // 2, device=DEV)
+        i0, i1 = (2 * half, 2 * half + 1) if case["inter"] else (half, half + rot // 2)
+        for b in range(B):
+            angle = s["pos"][b].double()[:, None] * s["inv_freq"][None]
+            c, sn = torch.cos(angle), torch.sin(angle)
+            for h in range(Hq + 2 * Hkv):
+                x = s["qkv"][b, :, h * d : (h + 1) * d].double()
+                w = s["qw"] if h < Hq else s["kw"]
+                if h < Hq + Hkv:
+                    if w is not None:
+                        x = x / torch.sqrt((x * x).sum(-1, keepdim=True) / d + 1e-6) * w.double()
+                    y = x.clone()
+                    y[:, i0] = x[:, i0] * c - x[:, i1] * sn
+                    y[:, i1] = x[:, i0] * sn + x[:, i1] * c
+                    x = y
+                out[b, h] = x
+        return out[:, :Hq].contiguous(), out[:, Hq : Hq + Hkv].contiguous(), out[:, Hq + Hkv :].contiguous()
+    page = case["page"]
+    if case["op"] == "write":  # the numbers that the stored ones round, in units of their row's power of two
+        outs = []
+        exps = []
+        for x, pool in ((s["k"], s["kp"]), (s["v"], s["vp"])):
+            y = torch.zeros(pool.shape, device=DEV, dtype=torch.float64)
+            e8 = torch.zeros(pool.shape[:3], device=DEV, dtype=torch.uint8)
+            for b in range(B):
+                n = int(s["count"][b])
+                at = int(s["start"][b]) + torch.arange(n, device=DEV)
+                pid = s["pages"][b].long()[at // page]
+                rows = x[b, :, :n].double().transpose(0, 1)  # [n, Hkv, d]
+                if case["e4m3"]:
+                    top = rows.abs().amax(-1)
+                    e = torch.ceil(torch.log2(top / 448.0)).clamp(min=-80.0)
+                    e = torch.where(torch.exp2(e) * 448.0 < top, e + 1, e)
+                    e = torch.where(torch.exp2(e - 1) * 448.0 >= top, e - 1, e).clamp(min=-80.0)
+                    e = torch.where(top == 0, 0.0, e)
+                    rows = rows / torch.exp2(e)[..., None]
+                    e8[pid, :, at % page] = (e + 127).to(torch.uint8)
+                y[pid, :, at % page] = rows
+            outs.append(y)
+            exps.append(e8 if case["e4m3"] else None)
+        return outs[0], outs[1], exps[0], exps[1]
+    if case["op"] == "read":
+        outs = []
+        for pool, ex in ((s["kp"], s["ke"]), (s["vp"], s["ve"])):
+            y = torch.zeros(B, Hkv, case["N"], d, device=DEV, dtype=torch.float64)
+            for b in range(B):
+                n = int(s["lens"][b])
+                for h in range(Hkv):
+                    y[b, h, :n] = _seq64(pool, ex, s["pages"][b], h, n)
+            outs.append(y)
+        return tuple(outs)
+    T, g = case["T"], Hq // Hkv
+    o = torch.zeros(B, Hq, T, d, device=DEV, dtype=torch.float64)
+    lse = torch.full((B, Hq, T), -math.inf, device=DEV, dtype=torch.float64)
+    for b in range(B):
+        ctx = int(s["ctx_lens"][b])
+        L = ctx + T
+        allowed = torch.ones(T, L, dtype=torch.bool)
+        for t in range(T):
+            for x in range(T):
+                allowed[t, ctx + x] = x <= t if s["mask"] is None else bool(int(s["mask"][b, t]) >> x & 1)
+        allowed = allowed.to(DEV)
+        for h in range(Hkv):
+            k, v = (_seq64(pool, ex, s["pages"][b], h, L) for pool, ex in ((s["kp"], s["ke"]), (s["vp"], s["ve"])))
+            for i in range(g):
+                x = torch.where(allowed, s["q"][b, h * g + i].double() @ k.T / math.sqrt(d), -math.inf)
+                lse[b, h * g + i] = torch.logsumexp(x, -1)
+                o[b, h * g + i] = torch.softmax(x, -1) @ v
+    return o, lse
