@@ -307,7 +307,7 @@ def _own_run(s):
     minf, cache, ws = _plan(s)
     if s["op"] == "rope":
         return minf.minf_qkv_norm_rope(s["qkv"], s["Hq"], s["Hkv"], pos=s["pos"], inv_freq=s["inv_freq"], q_weight=s["qw"],
-                                       k_weight=s["kw"], eps=1e-6, interleaved=s["inter"], ws=ws)
+                                       k_weight=s["kw"], eps=1e-6, interleaved=s["inter"])
     if s["op"] == "write":
         minf.minf_kv_write(s["k"], s["v"], cache, s["pages"], s["start"], count=s["count"], ws=ws)
         return s["kp"], s["vp"], s["ke"], s["ve"]
