@@ -1,0 +1,219 @@
+// The paged key-value cache: writing rows into it, as they are or in 8 bits,
+// and reading them back into the dense layout of the pre-fill calls.
+//
+// An 8-bit row holds e4m3 values times one power of two, 2^e with the smallest
+// e >= -80 for which max |x| <= 448 * 2^e (e = 0 for a row of zeros).  A power
+// of two keeps the division and the product exact, so the only rounding is
+// e4m3's own (at most 2^-4 of the value above 2^-6 * 2^e), what is read back
+// is exact in bf16, and attention can take the scale into an exponent.  The
+// scale costs one byte a row, e + 127; 255 marks a row that held a NaN or an
+// infinity, which reads back as NaN.
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "minf_device.cuh"
+#include "serve_internal.h"
+
+namespace minf {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // rows (of K and of V) that a lane group has in flight
+
+// Row index in the pools of position `at` of sequence b, or -1 with the error
+// reported: the position is outside the table or its page outside the pool.
+__device__ __forceinline__ long long pool_row(const KvView& c, int b, int h, long long at, DevStatus* st, int where) {
+  const long long pi = at >> c.log_page;
+  if (at < 0 || pi >= c.max_pages) {
+    report(st, MINF_ERR_DEVICE_BOUNDS, where);
+    return -1;
+  }
+  const int id = __ldg(c.pages + (long long)b * c.max_pages + pi);
+  if (id < 0 || id >= c.n_pages) {
+    report(st, MINF_ERR_DEVICE_BOUNDS, where + 1);
+    return -1;
+  }
+  return (((long long)id * c.Hkv + h) << c.log_page) + (at & ((1 << c.log_page) - 1));
+}
+
+// Eight bf16 of one lane to eight e4m3 bytes of the row's scale; every lane of
+// the row's L gets the row's stored exponent.
+template <int L>
+__device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& exp_byte) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t top = 0;  // max |x| as ordered bf16 bits
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int ex = (int)(top >> 7);                       // biased exponent
+  const int up = (top & 0x7fu) > 0x60u;                 // mantissa above 1.75 (448 = 1.75 * 2^8)
+  const int e = top == 0 ? 0 : max(ex - 135 + up, -80);
+  const bool bad = ex == 255;
+  exp_byte = bad ? 255u : (uint32_t)(e + 127);
+  const float s = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+  uint32_t out[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t two = w[2 * i + q];
+      const float2 f = make_float2(__uint_as_float(two << 16) * s, __uint_as_float(two & 0xffff0000u) * s);
+      v |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * q);
+    }
+    out[i] = bad ? 0x7f7f7f7fu : v;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+__device__ __forceinline__ uint4 dequantise8(const uint2& q, uint32_t exp_byte) {
+  const float s = exp_byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(exp_byte << 23);
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t two = (e < 2 ? q.x : q.y) >> (16 * (e & 1));
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    out[e] = pack_bf16x2(f.x * s, f.y * s);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// One row of K and one of V per group of D / 8 lanes, kUnroll of them in
+// flight; rows run over (batch, head, token), tokens fastest.
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p) {
+  constexpr int L = D / 8;
+  constexpr int kRows = kThreads / L;
+  const int lane = threadIdx.x % L, grp = threadIdx.x / L;
+  const int items = p.B * p.c.Hkv * p.N;
+  const int i0 = blockIdx.x * (kRows * kUnroll) + grp;
+  uint4 rk[kUnroll], rv[kUnroll];
+  long long dst[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long i = (long long)i0 + u * kRows;
+    dst[u] = -1;
+    rk[u] = rv[u] = make_uint4(0, 0, 0, 0);
+    if (i < items) {
+      const int n = (int)(i % p.N), bh = (int)(i / p.N);
+      const int h = bh % p.c.Hkv, b = bh / p.c.Hkv;
+      const int count = p.count ? __ldg(p.count + b) : p.N;
+      if (count < 0 || count > p.N) {
+        if (n == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 100);
+      } else if (n < count) {
+        const int src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
+        if (src < 0 || src >= p.M) {
+          report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
+        } else {
+          const int start = __ldg(p.start + b);
+          dst[u] = pool_row(p.c, b, h, start < 0 ? -1ll : (long long)start + n, p.status, 102);
+          rk[u] = __ldg(reinterpret_cast<const uint4*>(p.k + b * p.ksb + h * p.ksh + src * p.ksn) + lane);
+          rv[u] = __ldg(reinterpret_cast<const uint4*>(p.v + b * p.vsb + h * p.vsh + src * p.vsn) + lane);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    if constexpr (F8) {
+      uint32_t ek, ev;  // every lane of the warp takes part in the row maxima
+      const uint2 qk = quantise8<L>(rk[u], ek), qv = quantise8<L>(rv[u], ev);
+      if (dst[u] < 0) continue;
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.c.k) + dst[u] * D)[lane] = qk;
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.c.v) + dst[u] * D)[lane] = qv;
+      if (lane == 0) {
+        p.c.ke[dst[u]] = (uint8_t)ek;
+        p.c.ve[dst[u]] = (uint8_t)ev;
+      }
+    } else {
+      if (dst[u] < 0) continue;
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.k) + dst[u] * D)[lane] = rk[u];
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.v) + dst[u] * D)[lane] = rv[u];
+    }
+  }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p) {
+  constexpr int L = D / 8;
+  constexpr int kRows = kThreads / L;
+  const int lane = threadIdx.x % L, grp = threadIdx.x / L;
+  const int items = p.B * p.c.Hkv * p.N;
+  const int i0 = blockIdx.x * (kRows * kUnroll) + grp;
+  using Raw = typename std::conditional<F8, uint2, uint4>::type;
+  Raw rk[kUnroll], rv[kUnroll];
+  uint32_t ek[kUnroll], ev[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long i = (long long)i0 + u * kRows;
+    rk[u] = rv[u] = Raw{};
+    ek[u] = ev[u] = 127;
+    if (i < items) {
+      const int n = (int)(i % p.N), bh = (int)(i / p.N);
+      const int h = bh % p.c.Hkv, b = bh / p.c.Hkv;
+      if (n < __ldg(p.lens + b)) {
+        const long long row = pool_row(p.c, b, h, n, p.status, 104);
+        if (row >= 0) {
+          constexpr int kEl = F8 ? 1 : 2;
+          rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
+          rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
+          if constexpr (F8) {
+            ek[u] = __ldg(p.c.ke + row);
+            ev[u] = __ldg(p.c.ve + row);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long i = (long long)i0 + u * kRows;
+    if (i >= items) continue;
+    uint4 ok, ov;
+    if constexpr (F8) {
+      ok = dequantise8(rk[u], ek[u]);
+      ov = dequantise8(rv[u], ev[u]);
+    } else {
+      ok = rk[u];
+      ov = rv[u];
+    }
+    reinterpret_cast<uint4*>(p.k + i * D)[lane] = ok;
+    reinterpret_cast<uint4*>(p.v + i * D)[lane] = ov;
+  }
+}
+
+template <int D>
+int blocks_for(long long items) {
+  const int per = kThreads / (D / 8) * kUnroll;
+  return (int)((items + per - 1) / per);
+}
+
+}  // namespace
+
+cudaError_t kv_write_launch(int d, const KvWriteParams& p, cudaStream_t stream) {
+  const long long items = (long long)p.B * p.c.Hkv * p.N;
+  if (items == 0) return cudaSuccess;
+  if (d == 128 && p.c.ke) kv_write_kernel<128, true><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
+  else if (d == 128) kv_write_kernel<128, false><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
+  else if (d == 64 && p.c.ke) kv_write_kernel<64, true><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
+  else if (d == 64) kv_write_kernel<64, false><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
+  else return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+cudaError_t kv_read_launch(int d, const KvReadParams& p, cudaStream_t stream) {
+  const long long items = (long long)p.B * p.c.Hkv * p.N;
+  if (items == 0) return cudaSuccess;
+  if (d == 128 && p.c.ke) kv_read_kernel<128, true><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
+  else if (d == 128) kv_read_kernel<128, false><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
+  else if (d == 64 && p.c.ke) kv_read_kernel<64, true><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
+  else if (d == 64) kv_read_kernel<64, false><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
+  else return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+}  // namespace minf

@@ -26,7 +26,8 @@ EXPORTS = ["minf_vs_wmap_words", "minf_workspace_size", "minf_estimate_vs", "min
            "minf_build_index", "minf_sparse_attn_vs", "minf_sparse_attn_bs", "minf_attn_ashape",
            "minf_dense_attn", "minf_get_device_status", "minf_status_string", "minf_vs_bits_words",
            "minf_vs_twmap_words", "minf_build_index_exact", "minf_sparse_attn_vs_exact",
-           "minf_sparse_attn_layer", "minf_selftest_exp2", "minf_attn_grid"]
+           "minf_sparse_attn_layer", "minf_selftest_exp2", "minf_attn_grid", "minf_qkv_norm_rope", "minf_kv_write",
+           "minf_kv_read", "minf_tree_attn_workspace", "minf_tree_attn"]
 
 
 class MinfError(RuntimeError):
@@ -38,6 +39,11 @@ class MinfError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("N", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class _KVCacheC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")]
+                + [(n, ctypes.c_int) for n in ("n_pages", "Hkv", "page", "d", "type")])
 
 
 class _VsIndexC(ctypes.Structure):
@@ -86,13 +92,21 @@ def lib():
         L.minf_sparse_attn_layer.argtypes = [sp, vp, vp, vp, vp, i, ctypes.POINTER(_VsIndexC), i, i, vp, i, vp,
                                              vp, i, vp, i, i, i, vp, vp, vp, sz, vp]
         L.minf_attn_grid.argtypes = [sp, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, vp, sz, vp]
+        i64, cp = ctypes.c_int64, ctypes.POINTER(_KVCacheC)
+        L.minf_qkv_norm_rope.argtypes = [vp, i, i, i, i, i, i64, i64, vp, vp, i, i, vp, vp, ctypes.c_float,
+                                         vp, vp, vp, vp]
+        L.minf_kv_write.argtypes = [cp, vp, vp, i, i, i, vp, vp, vp, i, vp, vp, vp, vp, sz, vp]
+        L.minf_kv_read.argtypes = [cp, vp, i, i, vp, i, vp, vp, vp, sz, vp]
+        L.minf_tree_attn_workspace.argtypes = [i, i, i, i, i]
+        L.minf_tree_attn_workspace.restype = sz
+        L.minf_tree_attn.argtypes = [cp, vp, i, i, i, ctypes.c_float, vp, i, vp, vp, vp, vp, vp, vp, sz, vp]
         L.minf_get_device_status.argtypes = [vp, vp]
         L.minf_status_string.argtypes = [st]
         L.minf_status_string.restype = ctypes.c_char_p
         for fn in ("minf_estimate_vs", "minf_estimate_bs", "minf_build_index", "minf_sparse_attn_vs",
                    "minf_sparse_attn_bs", "minf_attn_ashape", "minf_dense_attn", "minf_get_device_status",
                    "minf_build_index_exact", "minf_sparse_attn_vs_exact", "minf_sparse_attn_layer",
-                   "minf_selftest_exp2"):
+                   "minf_selftest_exp2", "minf_qkv_norm_rope", "minf_kv_write", "minf_kv_read", "minf_tree_attn"):
             getattr(L, fn).restype = st
         _lib = L
     return _lib
@@ -432,3 +446,206 @@ def minf_selftest_exp2(x, stream=None):
     yp, ym = torch.empty_like(x), torch.empty_like(x)
     _check("minf_selftest_exp2", lib().minf_selftest_exp2(_p(x), _p(yp), _p(ym), x.numel(), _stream(stream)))
     return yp, ym
+
+
+# -------------------------------------------------------------------- serving
+# Entry points of include/minf.h's serving part.  Tensors are checked here
+# (type, shape, device, contiguity: a mismatch raises MinfError with "invalid
+# argument"), since the C ABI sees bare pointers.  A call runs on its tensors'
+# device, on that device's current stream unless `stream` says otherwise, and
+# allocates missing outputs there.
+E4M3 = torch.float8_e4m3fn
+
+
+def _need(ok, what):
+    if not ok:
+        raise MinfError(what, 1)
+
+
+def _ints(fn, name, t, shape, device, dtype=torch.int32):
+    """An index tensor of the given shape on `device`."""
+    if not (t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
+        raise MinfError(f"{fn} ({name}: contiguous {dtype} {list(shape)} on {device})", 1)
+
+
+def _dense(fn, name, t, shape, device, dtype=torch.bfloat16):
+    """A dense tensor of the given shape on `device`, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _ints(fn, name, t, shape, device, dtype)
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """Makes a tensor's device and the call's stream current while the call's
+    outputs are allocated and its kernels launched."""
+
+    def __init__(self, t, stream):
+        _need(t.is_cuda, "serving call (tensors in device memory)")
+        self.idx, self.stream = t.device.index, stream
+
+    def __enter__(self):
+        self.ctx = None
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.idx != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.idx)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def status_workspace(device="cuda"):
+    """The zeroed 256-byte workspace (status block) of the cache calls."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def tree_attn_workspace(B, Hq, Hkv, T, d, device="cuda"):
+    """A zeroed workspace for minf_tree_attn calls of up to this size."""
+    n = lib().minf_tree_attn_workspace(B, Hq, Hkv, T, d)
+    if n == 0:
+        raise MinfError("minf_tree_attn_workspace", 1)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+class KVCache:
+    """A paged key-value cache (see minf_kv_cache): k, v [n_pages, Hkv, page, d]
+    in bf16, or in torch.float8_e4m3fn with one exponent byte a row in k_exp,
+    v_exp [n_pages, Hkv, page]."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        f8 = k.dtype == E4M3
+        _need(k.dim() == 4 and v.shape == k.shape and v.dtype == k.dtype and v.device == k.device
+              and k.is_contiguous() and v.is_contiguous() and (f8 or k.dtype == torch.bfloat16),
+              "KVCache (k, v: contiguous [n_pages, Hkv, page, d], both bf16 or both float8_e4m3fn)")
+        _need(f8 == (k_exp is not None) and f8 == (v_exp is not None), "KVCache (k_exp and v_exp go with float8_e4m3fn)")
+        for e in (k_exp, v_exp) if f8 else ():
+            _need(e.dtype == torch.uint8 and e.shape == k.shape[:3] and e.is_contiguous() and e.device == k.device,
+                  "KVCache (k_exp, v_exp: contiguous uint8 [n_pages, Hkv, page])")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.n_pages, self.Hkv, self.page, self.d = k.shape
+        self.device = k.device
+        self._c = _KVCacheC(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), *k.shape, 1 if f8 else 0)
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def empty(n_pages, Hkv, page, d, e4m3=False, device="cuda"):
+        shape = (n_pages, Hkv, page, d)
+        k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=device) for _ in "kv")
+        if not e4m3:
+            return KVCache(k, v)
+        ke, ve = (torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in "kv")
+        return KVCache(k.view(E4M3), v.view(E4M3), ke, ve)
+
+
+def minf_qkv_norm_rope(qkv, Hq, Hkv, pos=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                       interleaved=False, want_v=True, q=None, k=None, v=None, stream=None):
+    """Projected rows qkv [B, N, (Hq + 2 Hkv) * d] (any batch and row strides that are multiples of 8) to
+    q [B, Hq, N, d], k and v [B, Hkv, N, d] (v is None without `want_v`), with the heads' norm and rotation
+    (see include/minf.h).  pos [B, N] int32, inv_freq [rot_dim / 2] float64, weights [d] bf16."""
+    fn = "minf_qkv_norm_rope"
+    _need(qkv.dtype == torch.bfloat16 and qkv.dim() == 3 and Hq > 0 and Hkv > 0 and
+          qkv.shape[2] % (Hq + 2 * Hkv) == 0 and qkv.stride(2) == 1, f"{fn} (qkv: bf16 [B, N, (Hq + 2 Hkv) * d])")
+    B, N, C = qkv.shape
+    d, dev = C // (Hq + 2 * Hkv), qkv.device
+    rot = 0
+    if pos is not None:
+        _ints(fn, "pos", pos, (B, N), dev)
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _ints(fn, "inv_freq", inv_freq, (rot // 2,), dev, torch.float64)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _ints(fn, name, w, (d,), dev, torch.bfloat16)
+    with _On(qkv, stream) as st:
+        q = _dense(fn, "q", q, (B, Hq, N, d), dev)
+        k = _dense(fn, "k", k, (B, Hkv, N, d), dev)
+        v = _dense(fn, "v", v, (B, Hkv, N, d), dev) if want_v or v is not None else None
+        row = qkv.stride(1) if N > 1 else max(C, qkv.stride(1))
+        _check(fn, lib().minf_qkv_norm_rope(
+            _ptr(qkv), B, N, Hq, Hkv, d, qkv.stride(0) if B > 1 else 0, row, _ptr(pos), _ptr(inv_freq), rot,
+            int(interleaved), _ptr(q_weight), _ptr(k_weight), eps, _ptr(q), _ptr(k), _ptr(v), st))
+    return q, k, v
+
+
+def _table(fn, cache, pages, B):
+    _need(pages.dim() == 2, f"{fn} (pages: [B, max_pages])")
+    _ints(fn, "pages", pages, (B, pages.shape[1]), cache.device)
+    return pages.shape[1]
+
+
+def minf_kv_write(k, v, cache: KVCache, pages, start, count=None, rows=None, ws=None, stream=None):
+    """Writes k, v [B, Hkv, M, d] (d contiguous, other strides multiples of 8) into the cache at positions
+    start[b] + i, i < count[b] (see include/minf.h); with `rows` [B, N] position start[b] + i gets row rows[b, i]."""
+    fn = "minf_kv_write"
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.bfloat16 and
+          k.device == v.device == cache.device and k.shape[1] == cache.Hkv and k.shape[3] == cache.d and
+          k.stride(3) == v.stride(3) == 1, f"{fn} (k, v: bf16 [B, Hkv, M, d] of the cache's Hkv, d and device)")
+    B, _, M, _ = k.shape
+    mp, dev = _table(fn, cache, pages, B), cache.device
+    _ints(fn, "start", start, (B,), dev)
+    if count is not None:
+        _ints(fn, "count", count, (B,), dev)
+    N = M
+    if rows is not None:
+        _need(rows.dim() == 2, f"{fn} (rows: [B, N])")
+        N = rows.shape[1]
+        _ints(fn, "rows", rows, (B, N), dev)
+    strides = [(ctypes.c_int64 * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))) for t in (k, v)]
+    with _On(k, stream) as st:
+        if ws is None:
+            ws = status_workspace(dev)
+        _check(fn, lib().minf_kv_write(cache._ref, _ptr(k), _ptr(v), B, N, M, strides[0], strides[1], _ptr(pages), mp,
+                                       _ptr(start), _ptr(count), _ptr(rows), _ptr(ws), ws.numel(), st))
+
+
+def minf_kv_read(cache: KVCache, pages, lens, N, k=None, v=None, ws=None, stream=None):
+    """Positions 0 .. N-1 of every sequence as dense bf16 k, v [B, Hkv, N, d], zeros from lens[b] on."""
+    fn = "minf_kv_read"
+    _need(pages.dim() == 2 and N >= 0, f"{fn} (pages: [B, max_pages], N >= 0)")
+    B, dev = pages.shape[0], cache.device
+    mp = _table(fn, cache, pages, B)
+    _ints(fn, "lens", lens, (B,), dev)
+    with _On(cache.k, stream) as st:
+        k = _dense(fn, "k", k, (B, cache.Hkv, N, cache.d), dev)
+        v = _dense(fn, "v", v, (B, cache.Hkv, N, cache.d), dev)
+        if ws is None:
+            ws = status_workspace(dev)
+        _check(fn, lib().minf_kv_read(cache._ref, _ptr(pages), B, mp, _ptr(lens), N, _ptr(k), _ptr(v), _ptr(ws),
+                                      ws.numel(), st))
+    return k, v
+
+
+def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=None, o=None, lse=None, want_lse=True,
+                   scale=0.0, ws=None, stream=None):
+    """Attention of the newest tokens q [B, Hq, T, d] over the cache, which holds their keys and values behind the
+    ctx_lens[b] context positions (see include/minf.h).  tree_mask [B, T] int64: bit u of word t lets token t see
+    token u; None is a chain.  n_draft [B] int32: tokens of each sequence (None: T); rows behind them are not
+    written (a new `o` is not initialised there)."""
+    fn = "minf_tree_attn"
+    _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.device == cache.device and
+          q.shape[3] == cache.d, f"{fn} (q: contiguous bf16 [B, Hq, T, d] of the cache's d and device)")
+    B, Hq, T, d = q.shape
+    mp, dev = _table(fn, cache, pages, B), cache.device
+    _ints(fn, "ctx_lens", ctx_lens, (B,), dev)
+    if n_draft is not None:
+        _ints(fn, "n_draft", n_draft, (B,), dev)
+    if tree_mask is not None:
+        _ints(fn, "tree_mask", tree_mask, (B, T), dev, torch.int64)
+    with _On(q, stream) as st:
+        o = _dense(fn, "o", o, (B, Hq, T, d), dev)
+        if want_lse or lse is not None:
+            lse = _dense(fn, "lse", lse, (B, Hq, T), dev, torch.float32)
+        if ws is None:
+            ws = tree_attn_workspace(B, Hq, cache.Hkv, T, d, dev)
+        _check(fn, lib().minf_tree_attn(cache._ref, _ptr(q), B, Hq, T, scale, _ptr(pages), mp, _ptr(ctx_lens),
+                                        _ptr(n_draft), _ptr(tree_mask), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), st))
+    return o, lse

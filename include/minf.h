@@ -398,6 +398,112 @@ minf_status minf_attn_grid(const minf_shape* shape, const minf_bf16* Q, const mi
                            const int32_t* heads, int nh, int frame_tokens, int k_b, int32_t* blk_idx,
                            int32_t* blk_cnt, minf_bf16* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving: what stands right before and right after pre-fill.  The projected
+ * rows of a layer become the Q, K and V that the calls above read; K and V go
+ * into a paged cache; new tokens (one, or a tree of drafted ones) attend over
+ * it; and a cached prefix comes back as dense K and V for the pre-fill of what
+ * follows it.  MInference covers pre-fill only and has no counterpart.
+ *
+ * These calls take any number of rows, not only multiples of 128.  Those that
+ * read device-resident ids or lengths take a workspace `ws`, zeroed once, whose
+ * first 256 bytes hold the status block described at the top; bad ids are
+ * skipped and set MINF_ERR_DEVICE_BOUNDS.  Calls that can run at the same time
+ * (other streams, or other graphs) need workspaces of their own.  Nothing is
+ * allocated and nothing synchronises, so every call can be captured into a
+ * graph; lengths, positions and page tables are read on the device when the
+ * call runs, so that a replayed graph follows them.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Head norm and position rotation of projected rows, in one pass that also
+ * brings them into the [B, H, N, d] layout.
+ *   X         rows of Hq query, Hkv key and Hkv value heads of d elements; row
+ *             n of batch b starts at X + b * batch_stride + n * row_stride
+ *             (elements, multiples of 8; 16-byte aligned)
+ *   q_weight, k_weight [d]: the query / key heads become x * w /
+ *             sqrt(mean(x^2) + eps); NULL: no norm of those heads
+ *   inv_freq  [rot_dim / 2] doubles: the first rot_dim elements (a multiple of
+ *             16, at most d) of every query and key head turn by the angle
+ *             position * inv_freq[i], taken in 64 bits; pair i is elements i and
+ *             i + rot_dim / 2, or 2i and 2i + 1 when `interleaved`.  NULL: no
+ *             rotation.
+ *   pos       [B, N] positions, or NULL for row n at position n
+ *   Q [B, Hq, N, d], K, V [B, Hkv, N, d]; V == NULL leaves the value heads out.
+ * 32-bit arithmetic, rounded once.  d in {64, 128}; N >= 0.  Q, K and V must
+ * not overlap X.
+ */
+minf_status minf_qkv_norm_rope(const minf_bf16* X, int B, int N, int Hq, int Hkv, int d, int64_t batch_stride,
+                               int64_t row_stride, const int32_t* pos, const double* inv_freq, int rot_dim,
+                               int interleaved, const minf_bf16* q_weight, const minf_bf16* k_weight, float eps,
+                               minf_bf16* Q, minf_bf16* K, minf_bf16* V, void* stream);
+
+/* Element types of a cache. */
+enum { MINF_KV_BF16 = 0, MINF_KV_E4M3 = 1 };
+
+/*
+ * A paged key-value cache, caller-owned device memory (16-byte aligned):
+ *   k, v   [n_pages, Hkv, page, d] bf16, or e4m3 bytes
+ *   k_exp, v_exp [n_pages, Hkv, page] (e4m3 only): a row's values are its bytes'
+ *          times 2^(exp - 127); 255 marks a row that held a NaN or an infinity
+ * page in {16, 32, 64, 128}, d in {64, 128}, n_pages * Hkv * page < 2^31.
+ * A batch's page table `pages` [B, max_pages] says where its sequences lie:
+ * position j of sequence b is row j % page of page pages[b, j / page].  Entries
+ * behind a sequence's end are not read.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int n_pages, Hkv, page, d;
+  int type; /* MINF_KV_* */
+} minf_kv_cache;
+
+/*
+ * Writes rows into the cache: row i < count[b] of the N of sequence b goes to
+ * position start[b] + i.  K and V have M source rows per head, element strides
+ * {batch, head, row} (multiples of 8; d contiguous); row i is source row
+ * rows[b, i], or i when rows is NULL (then M >= N).  count NULL means N.  With
+ * `rows`, the accepted tokens of a drafted tree go from its K and V to their
+ * final positions.  e4m3: a row's power of two is the smallest 2^e, e >= -80,
+ * with max |x| <= 448 * 2^e (2^0 for zeros), the values round to nearest even.
+ * Two rows of one call must not go to the same cache row.
+ */
+minf_status minf_kv_write(const minf_kv_cache* cache, const minf_bf16* K, const minf_bf16* V, int B, int N, int M,
+                          const int64_t* k_strides, const int64_t* v_strides, const int32_t* pages, int max_pages,
+                          const int32_t* start, const int32_t* count, const int32_t* rows, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * Reads the cache back: K and V [B, Hkv, N, d] bf16 get positions 0 .. N-1 of
+ * each sequence, zeros from position lens[b] on (lens[b] < 0 counts as 0; above
+ * N, N).  Exact: every cached value is a bf16 number.
+ */
+minf_status minf_kv_read(const minf_kv_cache* cache, const int32_t* pages, int B, int max_pages, const int32_t* lens,
+                         int N, minf_bf16* K, minf_bf16* V, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace that minf_tree_attn needs (0: bad arguments). */
+size_t minf_tree_attn_workspace(int B, int Hq, int Hkv, int T, int d);
+
+/*
+ * Attention of the T newest tokens of each sequence (1 <= T <= 64: one
+ * generated token, or a tree of drafted ones) over the cache, which already
+ * holds their own keys and values.  Q, O [B, Hq, T, d], lse [B, Hq, T] or NULL.
+ * Sequence b has ctx_lens[b] context positions, which every token sees, and
+ * behind them n_draft[b] <= T tokens (NULL: T).  Token t sees token u when bit
+ * u of tree_mask[b, t] is set; tree_mask NULL is a chain, u <= t.  Bits from
+ * n_draft[b] on are ignored.  A row that sees nothing gets O = 0 and lse =
+ * -inf; rows t >= n_draft[b] are not written.  scale <= 0 selects 1/sqrt(d).
+ * Scores, softmax and sums in 32 bits.  Cache rows outside what a sequence
+ * holds may contain anything.  The values of drafted tokens that a token does
+ * not see must be finite (their weight is zero, not skipped).
+ */
+minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B, int Hq, int T, float scale,
+                           const int32_t* pages, int max_pages, const int32_t* ctx_lens, const int32_t* n_draft,
+                           const uint64_t* tree_mask, minf_bf16* O, float* lse, void* ws, size_t ws_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
