@@ -1,7 +1,7 @@
 // Host side of the serving entry points of the libminf C ABI: argument checks,
 // workspace carving and dispatch.  See include/minf.h for their contracts.
 #include <cmath>
-#include <cstring>
+#include <mutex>
 
 #include "minf_device.cuh"
 #include "serve_internal.h"
@@ -49,6 +49,39 @@ bool strides_ok(const int64_t* s) {
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0 || s[i] % 8 != 0) return false;
   return true;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// A pool as [n_pages * Hkv * page, d] with boxes of one page by 128 bytes (64
+// with rows of 64 bytes), swizzled over that width.
+bool make_pool_map(CUtensorMap* m, void* ptr, const minf_kv_cache* c) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const bool f8 = c->type == MINF_KV_E4M3;
+  const int row_bytes = c->d * (f8 ? 1 : 2), box_bytes = row_bytes < 128 ? row_bytes : 128;
+  cuuint64_t dims[2] = {(cuuint64_t)c->d, (cuuint64_t)c->n_pages * c->Hkv * c->page};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)(f8 ? box_bytes : box_bytes / 2), (cuuint32_t)c->page};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -149,7 +182,8 @@ minf_status minf_kv_read(const minf_kv_cache* cache, const int32_t* pages, int B
 size_t minf_tree_attn_workspace(int B, int Hq, int Hkv, int T, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > 64 || (d != 64 && d != 128)) return 0;
   if ((long long)B * Hq * T >= (1ll << 31)) return 0;
-  return kStatusBytes + tree_part_floats(B, Hq, Hkv, T, d) * sizeof(float);
+  if (!tree_rows_supported(Hq, Hkv, T)) return 0;
+  return kStatusBytes + tree_part_floats(Hq, Hkv, T, d) * sizeof(float);
 }
 
 minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B, int Hq, int T, float scale,
@@ -160,7 +194,8 @@ minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B
   minf_status st = cache_view(cache, pages, B, max_pages, p.c);
   if (st != MINF_OK) return st;
   if (!Q || !O || !ctx_lens || Hq < 1 || Hq % cache->Hkv != 0 || T < 1) return MINF_ERR_INVALID_ARG;
-  if (T > 64) return MINF_ERR_UNSUPPORTED;
+  if (T > 64 || !tree_rows_supported(Hq, cache->Hkv, T) || (long long)B * cache->Hkv > 65535)
+    return MINF_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(O) || ((uintptr_t)tree_mask & 7)) return MINF_ERR_INVALID_ARG;
   if ((long long)B * Hq * T >= (1ll << 31)) return MINF_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, minf_tree_attn_workspace(B, Hq, cache->Hkv, T, cache->d))) != MINF_OK) return st;
@@ -177,7 +212,9 @@ minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt((float)cache->d)) * 1.4426950408889634f;
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kStatusBytes);
   p.status = reinterpret_cast<DevStatus*>(ws);
-  return cuda_status(tree_attn_launch(cache->d, p, (cudaStream_t)stream));
+  CUtensorMap tk, tv;
+  if (!make_pool_map(&tk, cache->k, cache) || !make_pool_map(&tv, cache->v, cache)) return MINF_ERR_CUDA;
+  return cuda_status(tree_attn_launch(cache->d, tk, tv, p, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,106 @@
+// Device primitives of the serving kernels beyond minf_device.cuh: 8-bit
+// tensor-core products, further operand layouts and TMEM access widths, a
+// wait that ends at once after an abort, and dependent launches.  Written
+// against the PTX ISA (tcgen05 / cp.async.bulk / griddepcontrol chapters).
+#pragma once
+
+#include "minf_device.cuh"
+
+namespace minf {
+
+// mbar_wait for roles that go on after a failure (their outputs are invalid and
+// the status says so): once *abort is set, a wait that is not over ends at once.
+__device__ __forceinline__ void mbar_wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, DevStatus* st,
+                                                   int where) {
+  if (mbar_test(bar, parity) || *abort) return;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
+    if (*abort) return;
+    if ((it & 63) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      report(st, MINF_ERR_DEVICE_TIMEOUT, where);
+      return;
+    }
+  }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Untiled bulk copy, global to shared (16-byte aligned addresses, size a multiple of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// D(tmem) (+)= A(smem) * B(smem), kind::f8f6f4 (8-bit inputs, fp32 accumulate).
+__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with fp32 D; A is e4m3, B e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int b_e5m2, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor; layout 0: no swizzle, 2: 128-byte, 4: 64-byte.
+// Unswizzled K-major: 16-byte columns `lbo` apart, 8-row groups `sbo` apart.
+// Unswizzled MN-major: 16-byte MN groups `sbo` apart, 8-row K groups `lbo` apart.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)layout << 61;
+}
+
+// 32 lanes x 16 consecutive 32-bit TMEM columns; valid after tmem_wait_ld().
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// C consecutive columns (16 or 32), complete on return.
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld16(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld32(taddr, r);
+  tmem_wait_ld();
+  reg_fence(r);
+}
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
+
+// Largest value over the warp's lanes; NaN counts as -infinity.  The float's bits
+// are made ordered as a signed integer, for the integer warp reduction.
+__device__ __forceinline__ float warp_max(float x) {
+  int k = __float_as_int(x == x ? x : -INFINITY);
+  k ^= (k >> 31) & 0x7fffffff;
+  k = __reduce_max_sync(0xFFFFFFFFu, k);
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// Lets the dependent launch begin; waits until the launch depended on is over
+// and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_prerequisite() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace minf

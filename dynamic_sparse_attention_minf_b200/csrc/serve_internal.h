@@ -69,8 +69,15 @@ struct TreeParams {
   float scale_log2;
   float* part;             // workspace
   DevStatus* status;
+  // set by the launch: row groups of `rows` rows, and the number and least
+  // length of the runs that the tile list is cut into
+  int groups, rows, lanes, min_run;
 };
-size_t tree_part_floats(int B, int Hq, int Hkv, int T, int d);
-cudaError_t tree_attn_launch(int d, const TreeParams& p, cudaStream_t stream);
+size_t tree_part_floats(int Hq, int Hkv, int T, int d);
+bool tree_rows_supported(int Hq, int Hkv, int T);
+// tk, tv: the pools as [n_pages * Hkv * page, d] with boxes of one page by 128
+// bytes (64 with rows of 64 bytes), swizzled over that width.
+cudaError_t tree_attn_launch(int d, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                             cudaStream_t stream);
 
 }  // namespace minf

@@ -2,159 +2,835 @@
 // drafted ones) over the paged key-value cache that already holds their keys
 // and values behind the context's.
 //
-// Row t of a sequence sees every key of the context, and the drafted key u when
-// bit u of its mask word is set.  Simple form: one block per row and split of
-// the keys, one warp per key at a time with the head spread over its lanes,
-// online softmax in 32 bits; a second kernel joins the splits in order.
+//   s = scale q.k,  O = sum_j 2^(s_j log2 e - m) v_j / l,  l = sum_j 2^(...)
+//
+// over the keys j that a row sees: the whole context, and the drafted key u when
+// bit u of the row's mask word is set.
+//
+// What bounds it is reading the cache once: a KV head's T * (Hq / Hkv) rows share
+// each key, so there are few operations per byte, and everything here serves to
+// keep loads in flight.
+//  * The products run transposed on the tensor cores, S^T = K Q^T and O^T =
+//    V^T P: the 128 keys of a tile (then the d elements of a value) are the 128
+//    rows of the instruction, and the query rows are its N = 16 .. 128 columns,
+//    so that one row costs 16 columns, not 128.  K and V tiles are used as TMA
+//    lays them down, in either element type.
+//  * A softmax thread owns a key: it sees the key's scores with every row, so a
+//    per-key scale is a thread's scalar, sums over keys stay in its registers
+//    until the end, and no maximum crosses lanes while the reference m holds.
+//    m is any value near the row's maximum: it is taken from the first tile and
+//    moves (with a rescaling of O^T and l) only when a score exceeds it by 2^16.
+//  * 8-bit keys and values enter the 8-bit product as they are.  The query row is
+//    brought to [128, 256) by a power of two and split into two e4m3 parts, which
+//    hold bf16's 8 bits; the weight (times the value's power of two) into three
+//    e5m2 parts, 9 bits, whose range of 2^32 keeps small weights beside a
+//    dominant one.
+//  * The tiles of all sequences and heads form one list, cut into equal runs, one
+//    per block: ragged batches and single long sequences both fill the GPU.  A
+//    run that covers part of a sequence leaves its sums in the workspace, and a
+//    second kernel, launched ahead of time, joins them in order.
 #include <cuda_fp8.h>
 
 #include <algorithm>
 
-#include "minf_device.cuh"
+#include "serve_device.cuh"
 #include "serve_internal.h"
 
 namespace minf {
 
 namespace {
 
-constexpr int kMaxSplits = 64;
+constexpr int kMaxBlocks = 148;  // one block per SM
+constexpr float kFloor = -1e30f; // reference of a row that has seen nothing
 
-int splits_for(long long rows) { return (int)std::max<long long>(1, std::min<long long>(kMaxSplits, 2368 / rows)); }
+// ------------------------------------------------------------------ partition
+__device__ __forceinline__ int new_tokens(const TreeParams& p, int b, int& ctx) {
+  ctx = __ldg(p.ctx + b);
+  const int nd = p.ndraft ? __ldg(p.ndraft + b) : p.T;
+  const bool ok = ctx >= 0 && nd >= 0 && nd <= p.T && (long long)ctx + nd <= ((long long)p.c.max_pages << p.c.log_page);
+  return ok ? nd : -1;
+}
+// 128-key tiles of one KV head of sequence b (0: no new tokens, or bad lengths)
+__device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
+  int ctx;
+  const int nd = new_tokens(p, b, ctx);
+  return nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+}
 
-struct Seq {
-  int ctx, nd, len;
-  bool ok;
+// Tiles before sequence b, and in all, of the warp's choice of b.
+__device__ __forceinline__ void warp_prefix(const TreeParams& p, int upto, long long& before, long long& total) {
+  const int lane = threadIdx.x & 31;
+  long long a = 0, t = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = tiles_of(p, b);
+    t += n;
+    if (b < upto) a += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  }
+  before = a * p.c.Hkv;
+  total = t * p.c.Hkv;
+}
+__device__ __forceinline__ long long run_length(const TreeParams& p, long long total) {
+  return max((long long)p.min_run, (total + p.lanes - 1) / p.lanes);
+}
+
+// A block's run [g, g1) of the tile list (sequence-major, then KV head, then
+// tile), walked one (sequence, head) segment at a time; every role of the block
+// walks it by itself.
+struct Walk {
+  long long g, g1, base;  // base: first tile of sequence b
+  int b, nt;              // nt: tiles per head of sequence b
+  // the current segment: tiles [t0, t1) of KV head h of sequence b
+  int h, t0, t1, ctx, nd;
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    if (g >= g1) return false;
+    while (g >= base + (long long)nt * p.c.Hkv) {
+      base += (long long)nt * p.c.Hkv;
+      ++b;
+      nt = tiles_of(p, b);
+    }
+    const long long x = g - base;
+    h = (int)(x / nt);
+    t0 = (int)(x % nt);
+    t1 = (int)min((long long)nt, t0 + (g1 - g));
+    nd = new_tokens(p, b, ctx);
+    g += t1 - t0;
+    return true;
+  }
 };
 
-// A sequence's lengths; a bad one counts as empty, and is reported by the caller.
-__device__ __forceinline__ Seq seq_of(const TreeParams& p, int b) {
-  Seq s;
-  s.ctx = __ldg(p.ctx + b);
-  s.nd = p.ndraft ? __ldg(p.ndraft + b) : p.T;
-  s.ok = s.ctx >= 0 && s.nd >= 0 && s.nd <= p.T &&
-         (long long)s.ctx + s.nd <= ((long long)p.c.max_pages << p.c.log_page);
-  s.len = s.ok ? s.ctx + s.nd : 0;
-  return s;
+// --------------------------------------------------------------------- layout
+template <int D, bool F8, int NR>
+struct Cfg {
+  static constexpr int kThreads = 320;                // two softmax warpgroups, issuer, producer
+  static constexpr int kRowB = D * (F8 ? 1 : 2);       // bytes of a cached row
+  static constexpr int kPitch = kRowB < 128 ? kRowB : 128;  // row pitch within a swizzled region
+  static constexpr int kRegions = kRowB / kPitch;
+  static constexpr int kRegion = 128 * kPitch;
+  static constexpr int kTileB = 128 * kRowB;
+  static constexpr int kQParts = F8 ? 2 : 1, kPParts = F8 ? 3 : 1;
+  static constexpr int kQPart = NR * kRowB;
+  static constexpr int kPPart = NR * 128 * (F8 ? 1 : 2);
+  static constexpr int kQB = kQParts * kQPart;
+  static constexpr int kPB = kPParts * kPPart;         // of one warpgroup
+  static constexpr int kMiscMax = 2 * NR * 4 + NR * 4 + (F8 ? NR * 4 : 0) + NR * 8 + 512;
+  static constexpr int kExpB = F8 ? 256 : 0;           // a tile's key and value exponents
+  static constexpr int kTiles = (232448 - kQB - 2 * kPB - kMiscMax - 8 * kExpB) / kTileB;
+  static constexpr int kKStages = (kTiles + 1) / 2 < 8 ? (kTiles + 1) / 2 : 8;
+  static constexpr int kVStages = kTiles / 2 < 8 ? kTiles / 2 : 8;
+  static constexpr int kOffV = 0;                      // the rings first: a 64-element V tile is read
+  static constexpr int kOffK = kOffV + kVStages * kTileB;  // past its end by the unused 64 output rows
+  static constexpr int kOffQ = kOffK + kKStages * kTileB;
+  static constexpr int kOffP = kOffQ + kQB;
+  static constexpr int kOffExp = kOffP + 2 * kPB;
+  static constexpr int kOffRef = kOffExp + kKStages * kExpB;  // [2][NR] references
+  static constexpr int kOffRow = kOffRef + 2 * NR * 4;        // [NR] row of the KV head's [group, T] queries
+  static constexpr int kOffFac = kOffRow + NR * 4;            // [NR] row factors (8-bit)
+  static constexpr int kOffWords = kOffFac + (F8 ? NR * 4 : 0);  // [NR] mask words
+  static constexpr int kOffBars = kOffWords + NR * 8;
+  // k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], pv_done[2], q_full, mma_done
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;    // TMEM slot, abort, the run
+  static constexpr int kSmem = kOffMisc + 48;
+  static constexpr uint32_t kSwizzle = kPitch == 128 ? 2u : 4u;
+  static constexpr uint32_t kGroup8 = 8 * kPitch;             // eight rows of a region
+  static constexpr int kTmem = 4 * NR;                        // S and O of two warpgroups
+  static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, NR, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
+  static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, NR, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
+  static constexpr int kCh = NR < 32 ? NR : 32;               // columns a thread takes at once
+  // the weights' references lie kOff below the maximum seen, so that 8-bit parts
+  // use the top of their range; a score kTop above the reference moves it
+  static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 16.f;
+  static_assert(kVStages >= 2 && kKStages >= 2, "rings");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(20 * NR <= kPB && 32 * NR <= kQB, "scratch in the idle P and Q buffers");
+  static_assert(NR * 512 <= 2 * kPB, "the joined output in the idle P buffers");
+};
+
+// A row's score and its mask.  y is the score in powers of two (with the value's
+// exponent, 8-bit), as -infinity where the row does not see the key.
+template <bool F8>
+__device__ __forceinline__ float score(uint32_t s, float km, float fac, float lv) {
+  return F8 ? fmaf(__uint_as_float(s) * km, fac, lv) : __uint_as_float(s) * fac;
+}
+
+// Sums each of N values (16 or 32) over the warp's lanes; lane i ends with the
+// total of value i (of value i / 2 when N is 16).
+template <int N>
+__device__ __forceinline__ float lane_totals(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int n = N;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float mine = up ? v[i + n] : v[i], other = up ? v[i] : v[i + n];
+          v[i] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    }
+  }
+  return v[0];
+}
+
+template <int D, bool F8, int NR>
+__global__ void __launch_bounds__(320, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const TreeParams p) {
+  using C = Cfg<D, F8, NR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part_lane = blockIdx.x / p.groups, rg = blockIdx.x % p.groups;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+  uint64_t* k_empty = k_full + C::kKStages;
+  uint64_t* v_full = k_empty + C::kKStages;
+  uint64_t* v_empty = v_full + C::kVStages;
+  uint64_t* s_full = v_empty + C::kVStages;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* q_full = pv_done + 2;
+  uint64_t* mma_done = q_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  Walk* start = reinterpret_cast<Walk*>(smem + C::kOffP);  // until the roles have copied it
+
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 112);
+    return;
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, C::kTmem < 32 ? 32 : C::kTmem);
+    tmem_relinquish();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      for (int s = 0; s < C::kKStages; ++s) {
+        mbar_init(&k_full[s], 1);
+        mbar_init(&k_empty[s], F8 ? 5 : 1);  // 8-bit: also the four warps that read the tile's exponents
+      }
+      for (int s = 0; s < C::kVStages; ++s) {
+        mbar_init(&v_full[s], 1);
+        mbar_init(&v_empty[s], 1);
+      }
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&s_full[w], 1);
+        mbar_init(&p_full[w], 128);
+        mbar_init(&pv_done[w], 1);
+      }
+      mbar_init(q_full, 256);
+      mbar_init(mma_done, 1);
+      *abort = 0;
+      fence_mbar_init();
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+  } else if (warp == 0) {
+    // this block's run of the tile list, and the sequence that it begins in
+    long long before, total;
+    warp_prefix(p, 0, before, total);
+    const long long per = run_length(p, total);
+    Walk w;
+    w.g = min(total, part_lane * per);
+    w.g1 = min(total, w.g + per);
+    w.base = 0;
+    w.b = 0;
+    w.nt = 0;
+    if (w.g < w.g1) {
+      for (int b0 = 0;; b0 += 32) {
+        const int n = b0 + lane < p.B ? tiles_of(p, b0 + lane) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + (long long)incl * p.c.Hkv > w.g);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          w.base += (long long)(__shfl_sync(0xFFFFFFFFu, incl, at) - __shfl_sync(0xFFFFFFFFu, n, at)) * p.c.Hkv;
+          w.b = b0 + at;
+          w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
+          break;
+        }
+        w.base += (long long)__shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
+      }
+    }
+    if (lane == 0) *start = w;
+    if (blockIdx.x == 0) {
+      for (int b = lane; b < p.B; b += 32) {
+        int ctx;
+        if (new_tokens(p, b, ctx) < 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  Walk w = *start;
+  __syncthreads();  // the run's place is the P buffer
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    int nk = 0, nv = 0;
+    // one tile's pages: lane i < pages loads page i
+    auto load_tile = [&](bool is_k, int row0, int pages) {
+      const int n = is_k ? nk : nv, stages = is_k ? C::kKStages : C::kVStages;
+      const int st = n % stages;
+      uint64_t* full = (is_k ? k_full : v_full) + st;
+      if (n >= stages)
+        mbar_wait_or_abort((is_k ? k_empty : v_empty) + st, ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
+      if (__any_sync(0xFFFFFFFFu, *abort)) return;
+      const int rows = pages << p.c.log_page;
+      if (lane == 0) mbar_arrive_expect_tx(full, rows * C::kRowB + (F8 && is_k ? 2 * rows : 0));
+      __syncwarp();
+      uint8_t* dst = smem + (is_k ? C::kOffK : C::kOffV) + st * C::kTileB + (lane << p.c.log_page) * C::kPitch;
+      if (lane < pages) {
+#pragma unroll
+        for (int r = 0; r < C::kRegions; ++r)
+          tma_load_2d(dst + r * C::kRegion, is_k ? &tmK : &tmV, full, r * 64, row0);
+        if (F8 && is_k) {
+          uint8_t* e = smem + C::kOffExp + st * 256 + (lane << p.c.log_page);
+          bulk_load(e, p.c.ke + row0, 1 << p.c.log_page, full);
+          bulk_load(e + 128, p.c.ve + row0, 1 << p.c.log_page, full);
+        }
+      }
+      __syncwarp();
+      (is_k ? nk : nv) = n + 1;
+    };
+    // failure-detection test hook: the first block withholds its key tiles, so its
+    // bounded waits run out and the call reports a timeout
+    bool live = p.status->withhold == 0 || blockIdx.x != 0;
+    while (live && w.next(p)) {
+      if (rg * NR >= w.nd * p.group) continue;
+      const int len = w.ctx + w.nd;
+      const int32_t* table = p.c.pages + (long long)w.b * p.c.max_pages;
+      const int per_tile = 128 >> p.c.log_page;
+      // first pool row of this lane's page of tile t; a bad page is reported and page 0 read instead
+      auto fetch = [&](int t, int& pages) {
+        pages = min(per_tile, (len - t * 128 + (1 << p.c.log_page) - 1) >> p.c.log_page);
+        int id = lane < pages ? __ldg(table + t * per_tile + lane) : 0;
+        if (id < 0 || id >= p.c.n_pages) {
+          report(p.status, MINF_ERR_DEVICE_BOUNDS, 111);
+          id = 0;
+        }
+        return (id * p.c.Hkv + w.h) << p.c.log_page;
+      };
+      int pages, row = fetch(w.t0, pages), pages_v = 0, row_v = 0;
+      for (int t = w.t0; t <= w.t1; ++t) {  // V trails K by one tile
+        int pages_n = 0, row_n = 0;
+        if (t + 1 < w.t1) row_n = fetch(t + 1, pages_n);
+        if (t < w.t1) load_tile(true, row, pages);
+        if (t > w.t0) load_tile(false, row_v, pages_v);
+        pages_v = pages;
+        row_v = row;
+        pages = pages_n;
+        row = row_n;
+        if (__any_sync(0xFFFFFFFFu, *abort)) {
+          live = false;
+          break;
+        }
+      }
+    }
+    if (lane == 0) {  // never exit with copies in flight
+      int dummy = 0;
+      for (int n = max(0, nk - C::kKStages); n < nk; ++n)
+        mbar_wait(&k_full[n % C::kKStages], (n / C::kKStages) & 1, &dummy, p.status, 115);
+      for (int n = max(0, nv - C::kVStages); n < nv; ++n)
+        mbar_wait(&v_full[n % C::kVStages], (n / C::kVStages) & 1, &dummy, p.status, 116);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // --------------------------------------------------------- MMA issuer
+    const uint32_t q0 = smem_u32(smem + C::kOffQ);
+    int it = 0, segs = 0;
+    // O^T of the tile's warpgroup (+)= V^T P
+    auto issue_pv = [&](int i, bool first) {
+      const int wg = i & 1, st = i % C::kVStages;
+      mbar_wait_or_abort(&p_full[wg], (i >> 1) & 1, abort, p.status, 117);
+      mbar_wait_or_abort(&v_full[st], (i / C::kVStages) & 1, abort, p.status, 118);
+      if (__any_sync(0xFFFFFFFFu, *abort)) return;
+      tc_fence_after();
+      const uint32_t v = smem_u32(smem + C::kOffV + st * C::kTileB), pb = smem_u32(smem + C::kOffP + wg * C::kPB);
+      const uint32_t d = tmem + 2 * NR + wg * NR;
+      if (elect_lane()) {
+#pragma unroll
+        for (int part = 0; part < C::kPParts; ++part)
+#pragma unroll
+          for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
+            constexpr int kKeys = F8 ? 32 : 16;
+            const uint64_t a = sdesc(v + kk * kKeys * C::kPitch, C::kRegion, C::kGroup8, C::kSwizzle);
+            const uint64_t b = sdesc(pb + part * C::kPPart + kk * kKeys * 16, 128, 2048, 0);
+            const uint32_t acc = part > 0 || kk > 0 || !first;
+            if constexpr (F8) umma_ss_f8(d, a, b, C::kIdescO, acc);
+            else umma_ss(d, a, b, C::kIdescO, acc);
+          }
+        umma_commit(&v_empty[st]);
+        umma_commit(&pv_done[wg]);
+      }
+      __syncwarp();
+    };
+    while (!__any_sync(0xFFFFFFFFu, *abort) && w.next(p)) {
+      if (rg * NR >= w.nd * p.group) continue;
+      mbar_wait_or_abort(q_full, segs & 1, abort, p.status, 119);
+      ++segs;
+      const int n = w.t1 - w.t0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int wg = it & 1, st = it % C::kKStages;
+        mbar_wait_or_abort(&k_full[st], (it / C::kKStages) & 1, abort, p.status, 120);
+        if (__any_sync(0xFFFFFFFFu, *abort)) break;
+        tc_fence_after();
+        const uint32_t k = smem_u32(smem + C::kOffK + st * C::kTileB);
+        if (elect_lane()) {
+#pragma unroll
+          for (int part = 0; part < C::kQParts; ++part)
+#pragma unroll
+            for (int kk = 0; kk < C::kRowB / 32; ++kk) {
+              const uint64_t a = sdesc(k + (kk * 32 / C::kPitch) * C::kRegion + (kk * 32) % C::kPitch, 16, C::kGroup8,
+                                       C::kSwizzle);
+              const uint64_t b = sdesc(q0 + part * C::kQPart + kk * 2 * NR * 16, NR * 16, 128, 0);
+              const uint32_t acc = part > 0 || kk > 0;
+              if constexpr (F8) umma_ss_f8(tmem + wg * NR, a, b, C::kIdescS, acc);
+              else umma_ss(tmem + wg * NR, a, b, C::kIdescS, acc);
+            }
+          umma_commit(&s_full[wg]);
+          umma_commit(&k_empty[st]);
+        }
+        __syncwarp();
+        if (i > 0) issue_pv(it - 1, i - 1 < 2);
+      }
+      if (!__any_sync(0xFFFFFFFFu, *abort)) issue_pv(it - 1, n - 1 < 2);
+    }
+    if (elect_lane()) umma_commit(mma_done);
+    __syncwarp();
+    if (lane == 0) {
+      int dummy = 0;
+      mbar_wait(mma_done, 0, &dummy, p.status, 121);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    // A failed wait is not followed up here: the status word and *abort are set,
+    // every later wait ends at once, and the barriers below keep their counts.
+    const int wg = warp >> 2, tid = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lanes + wg * NR, o_col = lanes + 2 * NR + wg * NR;
+    float* ref = reinterpret_cast<float*>(smem + C::kOffRef) + wg * NR;
+    float* ref_all = reinterpret_cast<float*>(smem + C::kOffRef);
+    float* fac = reinterpret_cast<float*>(smem + C::kOffFac);
+    int* row_at = reinterpret_cast<int*>(smem + C::kOffRow);
+    unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + C::kOffWords);
+    const uint32_t* words32 = reinterpret_cast<const uint32_t*>(words);
+    uint8_t* pbuf = smem + C::kOffP + wg * C::kPB;
+    float* wmax = reinterpret_cast<float*>(pbuf);           // [4][NR] while P is idle
+    float* shrink = wmax + 4 * NR;                          // [NR]
+    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ); // [2][4][NR] while Q is idle
+    float* stage = reinterpret_cast<float*>(smem + C::kOffP); // [NR][128] while P is idle
+    const int bar_wg = 1 + wg, bar_both = 3;
+    int it = 0, uses = 0;  // tiles of the block so far, and those of this warpgroup
+    while (w.next(p)) {
+      const int rows = min(NR, w.nd * p.group - rg * NR);
+      if (rows <= 0) continue;
+      const int len = w.ctx + w.nd, n = w.t1 - w.t0;
+      const long long qb = ((long long)w.b * p.Hq + w.h * p.group) * p.T;  // first query row of the KV head
+      // ---- the segment's queries, as the B operand; their mask words
+      if constexpr (!F8) {
+        for (int i = threadIdx.x; i < NR * (D / 8); i += 256) {
+          const int r = i % NR, c = i / NR;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
+            x = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + hq * p.T + t) * D) + c);
+          }
+          *reinterpret_cast<uint4*>(smem + C::kOffQ + c * NR * 16 + r * 16) = x;
+        }
+      } else {
+        constexpr int E = D / 32;
+        for (int r = warp; r < NR; r += 8) {
+          float x[E];
+          float top = 0.f;
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = 0.f;
+          if (r < rows) {
+            const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
+            const __nv_bfloat16* q = p.q + (qb + hq * p.T + t) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              x[e] = __bfloat162float(q[e]);
+              bad = bad || !(fabsf(x[e]) <= 3.4e38f);
+              top = fmaxf(top, fabsf(x[e]));
+            }
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          bad = __any_sync(0xFFFFFFFFu, bad);
+          // 2^up brings the largest to [128, 256)
+          const int up = top == 0.f ? 0 : min(100, 134 - (int)(__float_as_uint(top) >> 23));
+          const float s = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 a = make_float2(x[e] * s, x[e + 1] * s);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+            const uint32_t lo =
+                __nv_cvt_float2_to_fp8x2(make_float2(a.x - back.x, a.y - back.y), __NV_SATFINITE, __NV_E4M3);
+            const int byte = lane * E + e;
+            uint8_t* q = smem + C::kOffQ + (byte / 16) * NR * 16 + r * 16 + byte % 16;
+            *reinterpret_cast<uint16_t*>(q) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(q + C::kQPart) = (uint16_t)lo;
+          }
+          if (lane == 0) fac[r] = bad ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        }
+      }
+      for (int r = threadIdx.x; r < NR; r += 256) {
+        unsigned long long m = 0;
+        if (r < rows) {
+          const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
+          row_at[r] = hq * p.T + t;
+          m = p.mask ? p.mask[(long long)w.b * p.T + t] : (2ull << t) - 1;
+          if (w.nd < 64) m &= (1ull << w.nd) - 1;
+        }
+        words[r] = m;
+        ref_all[r] = ref_all[NR + r] = -INFINITY;
+      }
+      fence_proxy_async();
+      mbar_arrive(q_full);
+      named_bar_sync(bar_both, 256);
+
+      float l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) l[r] = 0.f;
+      bool first = true;
+      for (int i = 0; i < n; ++i, ++it) {
+        if ((it & 1) != wg) continue;
+        const int j0 = (w.t0 + i) * 128, j = j0 + tid, u = j - w.ctx;
+        const bool in = j < len;
+        const int kst = it % C::kKStages;
+        float km = 0.f, lv = 0.f, inv = 1.f;
+        if constexpr (F8) {
+          mbar_wait_or_abort(&k_full[kst], (it / C::kKStages) & 1, abort, p.status, 122);
+          const uint8_t* e = smem + C::kOffExp + kst * 256 + tid;
+          const uint32_t ke = e[0], ve = e[128];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_empty[kst]);
+          if (in) {
+            km = ke == 255u ? NAN : __uint_as_float(ke << 23);
+            lv = ve == 255u ? NAN : (float)((int)ve - 127);
+            inv = ve == 255u ? NAN : __uint_as_float((254u - ve) << 23);
+          }
+        }
+        mbar_wait_or_abort(&s_full[wg], uses & 1, abort, p.status, 123);
+        tc_fence_after();
+        auto tile = [&](auto masked) {
+          constexpr bool kMask = decltype(masked)::value;
+          auto sees = [&](int r) { return !kMask || (in && (u < 0 || (words32[2 * r + (u >> 5 & 1)] >> (u & 31) & 1))); };
+          uint32_t s[C::kCh];
+          auto y_of = [&](int c0, int c) {
+            const float y = score<F8>(s[c], km, F8 ? fac[c0 + c] : p.scale_log2, lv);
+            return sees(c0 + c) ? y : -INFINITY;
+          };
+          if (C::kCh == NR) tmem_get(s_col, s);
+          bool high = first;
+          if (!first) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+              if (C::kCh < NR) tmem_get(s_col + c0, s);
+#pragma unroll
+              for (int c = 0; c < C::kCh; ++c) top = fmaxf(top, y_of(c0, c) - ref[c0 + c]);
+            }
+            high = top > C::kTop;
+          }
+          if (!bar_and(bar_wg, 128, !high)) {
+            // move the references up to the largest scores seen; O^T and l follow
+            if (!first) {
+              mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 124);
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+              if (C::kCh < NR) tmem_get(s_col + c0, s);
+              float mine = 0.f;
+#pragma unroll
+              for (int c = 0; c < C::kCh; ++c) {
+                const float m = warp_max(y_of(c0, c));
+                if (c == lane) mine = m;
+              }
+              if (lane < C::kCh) wmax[(warp & 3) * NR + c0 + lane] = mine;
+            }
+            named_bar_sync(bar_wg, 128);
+            if (tid < NR) {
+              const float m = fmaxf(fmaxf(wmax[tid], wmax[NR + tid]), fmaxf(wmax[2 * NR + tid], wmax[3 * NR + tid]));
+              const float was = ref[tid], now = fmaxf(fmaxf(was, m - C::kOff), kFloor);
+              ref[tid] = now;
+              shrink[tid] = fast_exp2(was - now);
+            }
+            named_bar_sync(bar_wg, 128);
+            if (!first) {
+#pragma unroll
+              for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+                uint32_t o[C::kCh];
+                tmem_get(o_col + c0, o);
+#pragma unroll
+                for (int c = 0; c < C::kCh; ++c) {
+                  const float f = shrink[c0 + c];
+                  o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                  l[c0 + c] *= f;
+                }
+                tmem_put(o_col + c0, o);
+              }
+              tmem_wait_st();
+            }
+            named_bar_sync(bar_wg, 128);  // the scratch is the P buffer
+          } else {
+            mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 125);  // P is free
+          }
+          // the weights, to shared memory as the B operand: [NR / 16 bytes][128 keys][16 bytes]
+#pragma unroll
+          for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+            if (C::kCh < NR) tmem_get(s_col + c0, s);
+            constexpr int kStep = F8 ? 16 : 8;
+#pragma unroll
+            for (int g = 0; g < C::kCh; g += kStep) {
+              uint32_t out[C::kPParts][4];
+#pragma unroll
+              for (int c = 0; c < kStep; c += 2) {
+                const int r = c0 + g + c;
+                const float p0 = fast_exp2(y_of(c0, g + c) - ref[r]), p1 = fast_exp2(y_of(c0, g + c + 1) - ref[r + 1]);
+                if constexpr (F8) {
+                  l[r] = fmaf(p0, inv, l[r]);
+                  l[r + 1] = fmaf(p1, inv, l[r + 1]);
+                  __half2 h = __floats2half2_rn(p0, p1);  // e5m2 is the upper byte of a half
+#pragma unroll
+                  for (int q = 0; q < 3; ++q) {
+                    const uint32_t e =
+                        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E5M2);
+                    if (c & 2) out[q][c / 4] |= e << 16;
+                    else out[q][c / 4] = e;
+                    const uint32_t wide = __byte_perm(e, 0, 0x1404);
+                    h = __hsub2(h, *reinterpret_cast<const __half2*>(&wide));
+                  }
+                } else {
+                  l[r] += p0;
+                  l[r + 1] += p1;
+                  out[0][c / 2] = pack_bf16x2(p0, p1);
+                }
+              }
+#pragma unroll
+              for (int q = 0; q < C::kPParts; ++q)
+                *reinterpret_cast<uint4*>(pbuf + q * C::kPPart + (c0 + g) / kStep * 2048 + tid * 16) =
+                    make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
+            }
+          }
+          if (kMask && !in) {
+            // what lies behind the sequence's end may be anything: zero weight
+            // needs a finite value
+            const int st = it % C::kVStages;
+            mbar_wait_or_abort(&v_full[st], (it / C::kVStages) & 1, abort, p.status, 126);
+            uint8_t* v = smem + C::kOffV + st * C::kTileB + tid * C::kPitch;
+#pragma unroll
+            for (int x = 0; x < C::kRegions; ++x)
+#pragma unroll
+              for (int o = 0; o < C::kPitch; o += 16)
+                *reinterpret_cast<uint4*>(v + x * C::kRegion + o) = make_uint4(0, 0, 0, 0);
+          }
+        };
+        if (j0 + 128 > w.ctx) tile(std::true_type{});
+        else tile(std::false_type{});
+        first = false;
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&p_full[wg]);
+        ++uses;
+      }
+
+      // ---- the segment's end: sums over the keys, the two warpgroups joined
+      const bool some = !first;
+      if (some) {
+        mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 127);
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+          float v[C::kCh];
+#pragma unroll
+          for (int c = 0; c < C::kCh; ++c) v[c] = l[c0 + c];
+          const float t = lane_totals<C::kCh>(v);
+          if (C::kCh == 32) lsum[(wg * 4 + (warp & 3)) * NR + c0 + lane] = t;
+          else if ((lane & 1) == 0) lsum[(wg * 4 + (warp & 3)) * NR + lane / 2] = t;
+        }
+      }
+      named_bar_sync(bar_both, 256);
+      const bool has0 = n > 1 || ((it - 1) & 1) == 0, has1 = n > 1 || ((it - 1) & 1) == 1;
+      auto part_of = [&](int v, int r, float M) { return fast_exp2(ref_all[v * NR + r] - M); };
+      auto top_of = [&](int r) {
+        return fmaxf(has0 ? ref_all[r] : -INFINITY, has1 ? ref_all[NR + r] : -INFINITY);
+      };
+      if (wg == 1 && has1 && has0) {
+#pragma unroll
+        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+          uint32_t o[C::kCh];
+          tmem_get(o_col + c0, o);
+#pragma unroll
+          for (int c = 0; c < C::kCh; ++c) {
+            const int r = c0 + c;
+            stage[r * 128 + tid] = __uint_as_float(o[c]) * part_of(1, r, top_of(r));
+          }
+        }
+      }
+      if (has0 && has1) named_bar_sync(bar_both, 256);
+      if (wg == (has0 ? 0 : 1)) {
+        // whole: the segment covers all of the sequence's tiles
+        const bool whole = w.t0 == 0 && w.t1 == w.nt;
+        // where a partial segment's sums go: the block's first or second place
+        const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        float* part = p.part + slot * NR * (D + 2);
+#pragma unroll
+        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
+          uint32_t o[C::kCh];
+          tmem_get(o_col + c0, o);
+#pragma unroll
+          for (int c = 0; c < C::kCh; ++c) {
+            const int r = c0 + c;
+            if (r >= rows) continue;
+            const float M = top_of(r);
+            float a = __uint_as_float(o[c]), L = 0.f;
+            if (has0) {
+              const float f = part_of(0, r, M);
+              L += ((lsum[r] + lsum[NR + r]) + (lsum[2 * NR + r] + lsum[3 * NR + r])) * f;
+              a *= f;
+            }
+            if (has1) {
+              const float f = part_of(1, r, M);
+              L += ((lsum[4 * NR + r] + lsum[5 * NR + r]) + (lsum[6 * NR + r] + lsum[7 * NR + r])) * f;
+              if (has0) a += stage[r * 128 + tid];
+              else a *= f;
+            }
+            if (whole) {
+              const long long row = qb + row_at[r];
+              if (tid < D) p.o[row * D + tid] = __float2bfloat16(L == 0.f ? 0.f : a / L);
+              if (tid == 0 && p.lse)
+                p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+              if (tid < D) part[r * (D + 2) + tid] = a;
+              if (tid == 0) {
+                part[r * (D + 2) + D] = M;
+                part[r * (D + 2) + D + 1] = L;
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(bar_both, 256);  // Q, P and the references are the next segment's
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem < 32 ? 32 : C::kTmem);
+  }
+}
+
+// Joins the parts of the segments that several blocks shared, in the order of
+// their tiles: one block of D threads per row.
+template <int D>
+__global__ void __launch_bounds__(D) tree_join_kernel(const TreeParams p, int nr) {
+  const int bh = blockIdx.y, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
+  const int rg = blockIdx.x / nr, r = blockIdx.x % nr;  // nr rows of each row group
+  int ctx;
+  const int nd = new_tokens(p, b, ctx), nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+  long long before, total;
+  warp_prefix(p, b, before, total);
+  const long long per = run_length(p, total), s0 = before + (long long)h * nt, s1 = s0 + nt;
+  const int first = (int)(s0 / per), last = (int)((s1 - 1) / per);
+  wait_prerequisite();  // every block: the launches that follow rely on this one being over last
+  if (rg * nr + r >= nd * p.group || first >= last) return;
+  float M = -INFINITY;
+  auto part_of = [&](int i) {
+    const long long slot = 2ll * (i * p.groups + rg) + (i == first ? 1 : 0);
+    return p.part + (slot * p.rows + r) * (D + 2);
+  };
+  for (int i = first; i <= last; ++i) M = fmaxf(M, part_of(i)[D]);
+  float L = 0.f, a = 0.f;
+#pragma unroll 8
+  for (int i = first; i <= last; ++i) {
+    const float* x = part_of(i);
+    const float f = fast_exp2(x[D] - M);
+    L = fmaf(x[D + 1], f, L);
+    a = fmaf(x[threadIdx.x], f, a);
+  }
+  const int t = (rg * nr + r) / p.group, hq = (rg * nr + r) % p.group;
+  const long long row = ((long long)b * p.Hq + h * p.group + hq) * p.T + t;
+  p.o[row * D + threadIdx.x] = __float2bfloat16(L == 0.f ? 0.f : a / L);
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+int rows_per_block(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+template <int D, bool F8, int NR>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, cudaStream_t stream) {
+  using C = Cfg<D, F8, NR>;
+  const long long rows = (long long)p.T * p.group;
+  p.groups = (int)((rows + NR - 1) / NR);
+  p.rows = NR;
+  p.min_run = 2;
+  const long long most = (((long long)p.c.max_pages << p.c.log_page) + 127) / 128 * p.B * p.c.Hkv;
+  p.lanes = (int)std::max<long long>(1, std::min<long long>(kMaxBlocks / p.groups, (most + p.min_run - 1) / p.min_run));
+  const long long bh = (long long)p.B * p.c.Hkv;
+  if (p.groups > kMaxBlocks || bh > 65535) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  tree_attn_kernel<D, F8, NR><<<p.lanes * p.groups, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.groups * std::min<long long>(NR, rows)), (unsigned)bh);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p, (int)std::min<long long>(NR, rows));
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(128) tree_rows_kernel(const TreeParams p, int nsplit) {
-  constexpr int E = D / 32;  // elements per lane
-  const int row = blockIdx.y, split = blockIdx.x;
-  const int t = row % p.T, hq = row / p.T % p.Hq, b = row / p.T / p.Hq;
-  const int h = hq / p.group;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Seq s = seq_of(p, b);
-  if (!s.ok && threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
-  float* part = p.part + ((long long)row * nsplit + split) * (D + 2);
-  const unsigned long long mask = t < s.nd ? (p.mask ? p.mask[(long long)b * p.T + t] : (2ull << t) - 1) : 0ull;
-  float q[E], acc[E];
-  const __nv_bfloat16* qr = p.q + (long long)row * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qr[e]) * p.scale_log2;
-    acc[e] = 0.f;
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  switch (rows_per_block((long long)p.T * p.group)) {
+    case 16: return launch<D, F8, 16>(tk, tv, p, stream);
+    case 32: return launch<D, F8, 32>(tk, tv, p, stream);
+    case 64: return launch<D, F8, 64>(tk, tv, p, stream);
+    default: return launch<D, F8, 128>(tk, tv, p, stream);
   }
-  float m = -INFINITY, l = 0.f;
-  const int per = (s.len + nsplit - 1) / nsplit;
-  const int j1 = t < s.nd ? min(s.len, (split + 1) * per) : 0;
-  for (int j = split * per + warp; j < j1; j += 4) {
-    if (j >= s.ctx && !(mask >> (j - s.ctx) & 1)) continue;
-    const int id = __ldg(p.c.pages + (long long)b * p.c.max_pages + (j >> p.c.log_page));
-    if (id < 0 || id >= p.c.n_pages) {
-      if (lane == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 111);
-      continue;
-    }
-    const long long at = (((long long)id * p.c.Hkv + h) << p.c.log_page) + (j & ((1 << p.c.log_page) - 1));
-    float k[E], v[E];
-    if constexpr (F8) {
-      const uint32_t ke = p.c.ke[at], ve = p.c.ve[at];
-      const float ks = ke == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(ke << 23);
-      const float vs = ve == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(ve << 23);
-      const __nv_fp8_e4m3* kr = static_cast<const __nv_fp8_e4m3*>(p.c.k) + at * D + lane * E;
-      const __nv_fp8_e4m3* vr = static_cast<const __nv_fp8_e4m3*>(p.c.v) + at * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = (float)kr[e] * ks;
-        v[e] = (float)vr[e] * vs;
-      }
-    } else {
-      const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.c.k) + at * D + lane * E;
-      const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.c.v) + at * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = __bfloat162float(kr[e]);
-        v[e] = __bfloat162float(vr[e]);
-      }
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], k[e], x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    if (x == -INFINITY) continue;
-    const float m2 = x == x ? fmaxf(m, x) : x, f = exp2f(m - m2), w = exp2f(x - m2);
-    m = m2;
-    l = l * f + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e] * f);
-  }
-  __shared__ float sm[4][D + 2];
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    sm[warp][D] = m;
-    sm[warp][D + 1] = l;
-  }
-  __syncthreads();
-  float M = -INFINITY;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w][D]);
-  for (int i = threadIdx.x; i < D + 2; i += 128) {
-    float a = 0.f;
-    for (int w = 0; w < 4; ++w)
-      if (sm[w][D] != -INFINITY) a += sm[w][i] * exp2f(sm[w][D] - M);
-    part[i] = i == D ? M : a;
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(D) tree_join_kernel(const TreeParams p, int nsplit) {
-  const int row = blockIdx.x, t = row % p.T, b = row / p.T / p.Hq;
-  if (t >= seq_of(p, b).nd || !seq_of(p, b).ok) return;  // rows behind the last token stay as they were
-  const float* part = p.part + (long long)row * nsplit * (D + 2);
-  float M = -INFINITY, l = 0.f, a = 0.f;
-  for (int i = 0; i < nsplit; ++i) M = fmaxf(M, part[i * (D + 2) + D]);
-  for (int i = 0; i < nsplit; ++i) {
-    const float mi = part[i * (D + 2) + D];
-    if (mi == -INFINITY) continue;
-    const float f = exp2f(mi - M);
-    l += part[i * (D + 2) + D + 1] * f;
-    a += part[i * (D + 2) + threadIdx.x] * f;
-  }
-  p.o[(long long)row * D + threadIdx.x] = __float2bfloat16(M == -INFINITY ? 0.f : a / l);
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
-}
-
-template <int D>
-cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
-  const int rows = p.B * p.Hq * p.T, nsplit = splits_for(rows);
-  if (rows > 65535) return cudaErrorInvalidConfiguration;
-  if (p.c.ke) tree_rows_kernel<D, true><<<dim3(nsplit, rows), 128, 0, stream>>>(p, nsplit);
-  else tree_rows_kernel<D, false><<<dim3(nsplit, rows), 128, 0, stream>>>(p, nsplit);
-  tree_join_kernel<D><<<rows, D, 0, stream>>>(p, nsplit);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t tree_part_floats(int B, int Hq, int, int T, int d) {
-  const long long rows = (long long)B * Hq * T;
-  return (size_t)rows * splits_for(rows) * (d + 2);
+size_t tree_part_floats(int Hq, int Hkv, int T, int d) {
+  return 2ull * kMaxBlocks * rows_per_block((long long)T * (Hq / Hkv)) * (d + 2);
+}
+bool tree_rows_supported(int Hq, int Hkv, int T) {
+  const long long rows = (long long)T * (Hq / Hkv);
+  const int nr = rows_per_block(rows);
+  return (rows + nr - 1) / nr <= kMaxBlocks;
 }
 
-cudaError_t tree_attn_launch(int d, const TreeParams& p, cudaStream_t stream) {
-  if (d == 128) return launch<128>(p, stream);
-  if (d == 64) return launch<64>(p, stream);
+cudaError_t tree_attn_launch(int d, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                             cudaStream_t stream) {
+  if (d == 128) return p.c.ke ? launch_rows<128, true>(tk, tv, p, stream) : launch_rows<128, false>(tk, tv, p, stream);
+  if (d == 64) return p.c.ke ? launch_rows<64, true>(tk, tv, p, stream) : launch_rows<64, false>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 
