@@ -19,7 +19,9 @@
 //    per-key scale is a thread's scalar, sums over keys stay in its registers
 //    until the end, and no maximum crosses lanes while the reference m holds.
 //    m is any value near the row's maximum: it is taken from the first tile and
-//    moves (with a rescaling of O^T and l) only when a score exceeds it by 2^16.
+//    moves (with a rescaling of O^T and l) only when a score is 16 above it, in
+//    powers of two.  The weights are formed before that is known, and once more
+//    in the rare tile where it happens.
 //  * 8-bit keys and values enter the 8-bit product as they are.  The query row is
 //    brought to [128, 256) by a power of two and split into two e4m3 parts, which
 //    hold bf16's 8 bits; the weight (times the value's power of two) into three
@@ -32,6 +34,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "serve_device.cuh"
 #include "serve_internal.h"
@@ -141,22 +144,15 @@ struct Cfg {
   static constexpr int kTmem = 4 * NR;                        // S and O of two warpgroups
   static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, NR, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
   static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, NR, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
-  static constexpr int kCh = NR < 32 ? NR : 32;               // columns a thread takes at once
+  static constexpr int kCh = NR < 32 || NR == 128 ? 16 : 32;  // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
   static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(20 * NR <= kPB && 32 * NR <= kQB, "scratch in the idle P and Q buffers");
-  static_assert(NR * 512 <= 2 * kPB, "the joined output in the idle P buffers");
+  static_assert(24 * NR <= kPB && 40 * NR <= kQB, "scratch in the idle P and Q buffers");
+  static_assert(NR * D * 2 <= 2 * kPB, "the queries as they are in the idle P buffers");
 };
-
-// A row's score and its mask.  y is the score in powers of two (with the value's
-// exponent, 8-bit), as -infinity where the row does not see the key.
-template <bool F8>
-__device__ __forceinline__ float score(uint32_t s, float km, float fac, float lv) {
-  return F8 ? fmaf(__uint_as_float(s) * km, fac, lv) : __uint_as_float(s) * fac;
-}
 
 // Sums each of N values (16 or 32) over the warp's lanes; lane i ends with the
 // total of value i (of value i / 2 when N is 16).
@@ -282,27 +278,28 @@ __global__ void __launch_bounds__(320, 1)
   if (warp == 9) {
     // ------------------------------------------------------------ producer
     int nk = 0, nv = 0;
-    // one tile's pages: lane i < pages loads page i
-    auto load_tile = [&](bool is_k, int row0, int pages) {
+    // One tile's pages: lane i < pages loads page i.  With K go, in 8 bits, the
+    // exponents of the tile's keys and values, four keys per lane.
+    auto load_tile = [&](bool is_k, int row0, int pages, uint32_t ke, uint32_t ve) {
       const int n = is_k ? nk : nv, stages = is_k ? C::kKStages : C::kVStages;
       const int st = n % stages;
       uint64_t* full = (is_k ? k_full : v_full) + st;
       if (n >= stages)
         mbar_wait_or_abort((is_k ? k_empty : v_empty) + st, ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
       if (__any_sync(0xFFFFFFFFu, *abort)) return;
-      const int rows = pages << p.c.log_page;
-      if (lane == 0) mbar_arrive_expect_tx(full, rows * C::kRowB + (F8 && is_k ? 2 * rows : 0));
+      if (F8 && is_k) {
+        uint32_t* e = reinterpret_cast<uint32_t*>(smem + C::kOffExp + st * C::kExpB) + lane;
+        e[0] = ke;
+        e[32] = ve;
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive_expect_tx(full, (pages << p.c.log_page) * C::kRowB);
       __syncwarp();
       uint8_t* dst = smem + (is_k ? C::kOffK : C::kOffV) + st * C::kTileB + (lane << p.c.log_page) * C::kPitch;
       if (lane < pages) {
 #pragma unroll
         for (int r = 0; r < C::kRegions; ++r)
           tma_load_2d(dst + r * C::kRegion, is_k ? &tmK : &tmV, full, r * 64, row0);
-        if (F8 && is_k) {
-          uint8_t* e = smem + C::kOffExp + st * 256 + (lane << p.c.log_page);
-          bulk_load(e, p.c.ke + row0, 1 << p.c.log_page, full);
-          bulk_load(e + 128, p.c.ve + row0, 1 << p.c.log_page, full);
-        }
       }
       __syncwarp();
       (is_k ? nk : nv) = n + 1;
@@ -325,16 +322,34 @@ __global__ void __launch_bounds__(320, 1)
         }
         return (id * p.c.Hkv + w.h) << p.c.log_page;
       };
-      int pages, row = fetch(w.t0, pages), pages_v = 0, row_v = 0;
-      for (int t = w.t0; t <= w.t1; ++t) {  // V trails K by one tile
-        int pages_n = 0, row_n = 0;
-        if (t + 1 < w.t1) row_n = fetch(t + 1, pages_n);
-        if (t < w.t1) load_tile(true, row, pages);
-        if (t > w.t0) load_tile(false, row_v, pages_v);
+      auto exponents = [&](int row, int pages, uint32_t& ke, uint32_t& ve) {
+        const int pg = (4 * lane) >> p.c.log_page;
+        const int at = __shfl_sync(0xFFFFFFFFu, row, pg) + ((4 * lane) & ((1 << p.c.log_page) - 1));
+        ke = ve = 0;
+        if (F8 && pg < pages) {
+          ke = __ldg(reinterpret_cast<const uint32_t*>(p.c.ke + at));
+          ve = __ldg(reinterpret_cast<const uint32_t*>(p.c.ve + at));
+        }
+      };
+      // page ids are read two tiles ahead, exponents one; V trails K by one tile
+      int pages = 0, row = fetch(w.t0, pages), pages_n = 0, row_n = 0, pages_v = 0, row_v = 0;
+      uint32_t ke, ve, ke_n = 0, ve_n = 0;
+      if (w.t0 + 1 < w.t1) row_n = fetch(w.t0 + 1, pages_n);
+      exponents(row, pages, ke, ve);
+      for (int t = w.t0; t <= w.t1; ++t) {
+        int pages_2 = 0, row_2 = 0;
+        if (t + 2 < w.t1) row_2 = fetch(t + 2, pages_2);
+        exponents(row_n, pages_n, ke_n, ve_n);
+        if (t < w.t1) load_tile(true, row, pages, ke, ve);
+        if (t > w.t0) load_tile(false, row_v, pages_v, 0, 0);
         pages_v = pages;
         row_v = row;
         pages = pages_n;
         row = row_n;
+        pages_n = pages_2;
+        row_n = row_2;
+        ke = ke_n;
+        ve = ve_n;
         if (__any_sync(0xFFFFFFFFu, *abort)) {
           live = false;
           break;
@@ -424,17 +439,19 @@ __global__ void __launch_bounds__(320, 1)
     const int wg = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lanes + wg * NR, o_col = lanes + 2 * NR + wg * NR;
-    float* ref = reinterpret_cast<float*>(smem + C::kOffRef) + wg * NR;
-    float* ref_all = reinterpret_cast<float*>(smem + C::kOffRef);
+    // the references, negated: [2][NR]
+    float* nref_all = reinterpret_cast<float*>(smem + C::kOffRef);
+    float* nref = nref_all + wg * NR;
     float* fac = reinterpret_cast<float*>(smem + C::kOffFac);
     int* row_at = reinterpret_cast<int*>(smem + C::kOffRow);
     unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + C::kOffWords);
     const uint32_t* words32 = reinterpret_cast<const uint32_t*>(words);
     uint8_t* pbuf = smem + C::kOffP + wg * C::kPB;
-    float* wmax = reinterpret_cast<float*>(pbuf);           // [4][NR] while P is idle
-    float* shrink = wmax + 4 * NR;                          // [NR]
-    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ); // [2][4][NR] while Q is idle
-    float* stage = reinterpret_cast<float*>(smem + C::kOffP); // [NR][128] while P is idle
+    float* wmax = reinterpret_cast<float*>(pbuf);             // [4][NR] while P is idle
+    float* shrink = wmax + 4 * NR;                            // [NR]
+    float* nwas = shrink + NR;                                // [NR]
+    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ);  // [2][4][NR] while Q is idle
+    float* weight = lsum + 8 * NR;                            // [2][NR]
     const int bar_wg = 1 + wg, bar_both = 3;
     int it = 0, uses = 0;  // tiles of the block so far, and those of this warpgroup
     while (w.next(p)) {
@@ -443,36 +460,56 @@ __global__ void __launch_bounds__(320, 1)
       const int len = w.ctx + w.nd, n = w.t1 - w.t0;
       const long long qb = ((long long)w.b * p.Hq + w.h * p.group) * p.T;  // first query row of the KV head
       // ---- the segment's queries, as the B operand; their mask words
-      if constexpr (!F8) {
-        for (int i = threadIdx.x; i < NR * (D / 8); i += 256) {
-          const int r = i % NR, c = i / NR;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
-            x = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + hq * p.T + t) * D) + c);
-          }
-          *reinterpret_cast<uint4*>(smem + C::kOffQ + c * NR * 16 + r * 16) = x;
+#pragma unroll 1
+      for (int r = threadIdx.x; r < NR; r += 256) {
+        unsigned long long m = 0;
+        if (r < rows) {
+          const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
+          row_at[r] = hq * p.T + t;
+          m = p.mask ? p.mask[(long long)w.b * p.T + t] : (2ull << t) - 1;
+          if (w.nd < 64) m &= (1ull << w.nd) - 1;
         }
-      } else {
+        words[r] = m;
+        nref_all[r] = nref_all[NR + r] = INFINITY;
+      }
+      named_bar_sync(bar_both, 256);
+      {
+        // 16-byte pieces: bf16 queries go where the product reads them, 8-bit ones
+        // are staged in the P buffer (rows of D) and split below
+        constexpr int kPieces = NR * (D / 8) / 256 > 0 ? NR * (D / 8) / 256 : 1;
+        uint4 x[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int id = i * 256 + threadIdx.x, r = id % NR, c = id / NR;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (id < NR * (D / 8) && r < rows)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + row_at[r]) * D) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int id = i * 256 + threadIdx.x, r = id % NR, c = id / NR;
+          if (id < NR * (D / 8))
+            *reinterpret_cast<uint4*>(smem + (F8 ? C::kOffP + r * D * 2 + c * 16 : C::kOffQ + c * NR * 16 + r * 16)) = x[i];
+        }
+      }
+      if constexpr (F8) {
+        named_bar_sync(bar_both, 256);
         constexpr int E = D / 32;
+#pragma unroll 1
         for (int r = warp; r < NR; r += 8) {
           float x[E];
           float top = 0.f;
           bool bad = false;
+          const __nv_bfloat162* q2 = reinterpret_cast<const __nv_bfloat162*>(smem + C::kOffP + r * D * 2) + lane * (E / 2);
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = 0.f;
-          if (r < rows) {
-            const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
-            const __nv_bfloat16* q = p.q + (qb + hq * p.T + t) * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              x[e] = __bfloat162float(q[e]);
-              bad = bad || !(fabsf(x[e]) <= 3.4e38f);
-              top = fmaxf(top, fabsf(x[e]));
-            }
+          for (int e = 0; e < E; e += 2) {
+            const float2 f = __bfloat1622float2(q2[e / 2]);
+            x[e] = f.x;
+            x[e + 1] = f.y;
+            bad = bad || !(fabsf(f.x) <= 3.4e38f) || !(fabsf(f.y) <= 3.4e38f);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          top = warp_max(top);
           bad = __any_sync(0xFFFFFFFFu, bad);
           // 2^up brings the largest to [128, 256)
           const int up = top == 0.f ? 0 : min(100, 134 - (int)(__float_as_uint(top) >> 23));
@@ -492,34 +529,24 @@ __global__ void __launch_bounds__(320, 1)
           if (lane == 0) fac[r] = bad ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
         }
       }
-      for (int r = threadIdx.x; r < NR; r += 256) {
-        unsigned long long m = 0;
-        if (r < rows) {
-          const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
-          row_at[r] = hq * p.T + t;
-          m = p.mask ? p.mask[(long long)w.b * p.T + t] : (2ull << t) - 1;
-          if (w.nd < 64) m &= (1ull << w.nd) - 1;
-        }
-        words[r] = m;
-        ref_all[r] = ref_all[NR + r] = -INFINITY;
-      }
       fence_proxy_async();
       mbar_arrive(q_full);
       named_bar_sync(bar_both, 256);
 
-      float l[NR];
+      uint64_t l[NR / 2];  // this key lane's sums of two rows each
 #pragma unroll
-      for (int r = 0; r < NR; ++r) l[r] = 0.f;
+      for (int r = 0; r < NR / 2; ++r) l[r] = 0ull;
       bool first = true;
+#pragma unroll 1
       for (int i = 0; i < n; ++i, ++it) {
         if ((it & 1) != wg) continue;
         const int j0 = (w.t0 + i) * 128, j = j0 + tid, u = j - w.ctx;
         const bool in = j < len;
         const int kst = it % C::kKStages;
-        float km = 0.f, lv = 0.f, inv = 1.f;
+        float km = 0.f, lv = 0.f, inv = 1.f;  // 2^key exponent, value exponent, its inverse power
         if constexpr (F8) {
           mbar_wait_or_abort(&k_full[kst], (it / C::kKStages) & 1, abort, p.status, 122);
-          const uint8_t* e = smem + C::kOffExp + kst * 256 + tid;
+          const uint8_t* e = smem + C::kOffExp + kst * C::kExpB + tid;
           const uint32_t ke = e[0], ve = e[128];
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_empty[kst]);
@@ -531,108 +558,149 @@ __global__ void __launch_bounds__(320, 1)
         }
         mbar_wait_or_abort(&s_full[wg], uses & 1, abort, p.status, 123);
         tc_fence_after();
+        // From the tile's scores s to the exponents of their weights, two rows at a
+        // time: s scale log2(e) + lv - reference, -infinity where the row does not
+        // see the key.
+        auto exponent2 = [&](auto masked, uint32_t s0, uint32_t s1, int r, const float* minus, float& t0, float& t1) {
+          const uint64_t s2 = f32x2_pack(__uint_as_float(s0), __uint_as_float(s1));
+          const float2 m = *reinterpret_cast<const float2*>(minus + r);
+          if constexpr (F8) {
+            const float2 f = *reinterpret_cast<const float2*>(fac + r);
+            f32x2_unpack(f32x2_fma(f32x2_mul(s2, f32x2_pack(km, km)), f32x2_pack(f.x, f.y),
+                                   f32x2_add(f32x2_pack(lv, lv), f32x2_pack(m.x, m.y))),
+                         t0, t1);
+          } else {
+            f32x2_unpack(f32x2_fma(s2, f32x2_pack(p.scale_log2, p.scale_log2), f32x2_pack(m.x, m.y)), t0, t1);
+          }
+          if constexpr (decltype(masked)::value) {
+            const int wd = u >> 5 & 1, bit = u & 31;
+            t0 = in && (u < 0 || (words32[2 * r + wd] >> bit & 1)) ? t0 : -INFINITY;
+            t1 = in && (u < 0 || (words32[2 * r + 2 + wd] >> bit & 1)) ? t1 : -INFINITY;
+          }
+        };
         auto tile = [&](auto masked) {
-          constexpr bool kMask = decltype(masked)::value;
-          auto sees = [&](int r) { return !kMask || (in && (u < 0 || (words32[2 * r + (u >> 5 & 1)] >> (u & 31) & 1))); };
-          uint32_t s[C::kCh];
-          auto y_of = [&](int c0, int c) {
-            const float y = score<F8>(s[c], km, F8 ? fac[c0 + c] : p.scale_log2, lv);
-            return sees(c0 + c) ? y : -INFINITY;
-          };
-          if (C::kCh == NR) tmem_get(s_col, s);
-          bool high = first;
-          if (!first) {
+          bool move = first;
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            if (move) {
+              // move the references up to the largest scores seen; O^T and l follow
+              if (!first) {
+                mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 124);
+                tc_fence_after();
+                named_bar_sync(bar_wg, 128);
+              }
+              if (tid < NR) nwas[tid] = first ? 0.f : nref[tid];
+              named_bar_sync(bar_wg, 128);
+#pragma unroll 1
+              for (int c0 = 0; c0 < NR; c0 += 8) {
+                uint32_t s[8];
+                tmem_ld(s_col + c0, s);
+                tmem_landed(s);
+                float mine = 0.f;
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                  float t0, t1;
+                  exponent2(masked, s[c], s[c + 1], c0 + c, nwas, t0, t1);
+                  t0 = warp_max(t0);
+                  t1 = warp_max(t1);
+                  if (lane == c) mine = t0;
+                  if (lane == c + 1) mine = t1;
+                }
+                if (lane < 8) wmax[(warp & 3) * NR + c0 + lane] = mine;
+              }
+              named_bar_sync(bar_wg, 128);
+              if (tid < NR) {
+                // the largest, above the former reference (above 0 in the first tile)
+                const float up = fmaxf(fmaxf(wmax[tid], wmax[NR + tid]), fmaxf(wmax[2 * NR + tid], wmax[3 * NR + tid])) -
+                                 C::kOff;
+                if (first) {
+                  nref[tid] = -fmaxf(up, kFloor);
+                } else {
+                  const float now = fmaxf(-nwas[tid] + up, -nwas[tid]);
+                  nref[tid] = -now;
+                  shrink[tid] = fast_exp2(-nwas[tid] - now);
+                }
+              }
+              named_bar_sync(bar_wg, 128);
+              if (!first) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < NR; c0 += 8) {
+                  uint32_t o[8];
+                  tmem_ld(o_col + c0, o);
+                  tmem_landed(o);
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * shrink[c0 + c]);
+                  tmem_st(o_col + c0, o);
+                }
+                tmem_wait_st();
+                // l without the weights that the first pass added: they are formed
+                // again.  Below 2^-90 what was there before them does not count.
+#pragma unroll
+                for (int c0 = 0; c0 < NR; c0 += 16) {
+                  uint32_t s[16];
+                  tmem_ld(s_col + c0, s);
+                  tmem_landed(s);
+#pragma unroll
+                  for (int c = 0; c < 16; c += 2) {
+                    const int r = c0 + c;
+                    float t0, t1, l0, l1;
+                    exponent2(masked, s[c], s[c + 1], r, nwas, t0, t1);
+                    f32x2_unpack(l[r / 2], l0, l1);
+                    l0 = shrink[r] < 0x1p-90f ? 0.f : (l0 - fast_exp2(t0) * inv) * shrink[r];
+                    l1 = shrink[r + 1] < 0x1p-90f ? 0.f : (l1 - fast_exp2(t1) * inv) * shrink[r + 1];
+                    l[r / 2] = f32x2_pack(l0, l1);
+                  }
+                }
+              }
+              named_bar_sync(bar_wg, 128);  // the scratch is the P buffer
+            }
+            // the weights, to shared memory as the B operand: [NR / 16 bytes][128 keys][16 bytes]
+            if (!first && pass == 0) mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 125);  // P is free
             float top = -INFINITY;
 #pragma unroll
             for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-              if (C::kCh < NR) tmem_get(s_col + c0, s);
+              uint32_t s[C::kCh];
+              tmem_ld(s_col + c0, s);
+              tmem_landed(s);
+              constexpr int kStep = F8 ? 16 : 8;
 #pragma unroll
-              for (int c = 0; c < C::kCh; ++c) top = fmaxf(top, y_of(c0, c) - ref[c0 + c]);
-            }
-            high = top > C::kTop;
-          }
-          if (!bar_and(bar_wg, 128, !high)) {
-            // move the references up to the largest scores seen; O^T and l follow
-            if (!first) {
-              mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 124);
-              tc_fence_after();
-            }
+              for (int g = 0; g < C::kCh; g += kStep) {
+                uint32_t out[C::kPParts][4];
 #pragma unroll
-            for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-              if (C::kCh < NR) tmem_get(s_col + c0, s);
-              float mine = 0.f;
+                for (int c = 0; c < kStep; c += 2) {
+                  const int r = c0 + g + c;
+                  float t0, t1;
+                  exponent2(masked, s[g + c], s[g + c + 1], r, nref, t0, t1);
+                  top = fmaxf(top, fmaxf(t0, t1));
+                  const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                  if constexpr (F8) {
+                    l[r / 2] = f32x2_fma(f32x2_pack(p0, p1), f32x2_pack(inv, inv), l[r / 2]);
+                    __half2 h = __floats2half2_rn(p0, p1);  // e5m2 is the upper byte of a half
 #pragma unroll
-              for (int c = 0; c < C::kCh; ++c) {
-                const float m = warp_max(y_of(c0, c));
-                if (c == lane) mine = m;
-              }
-              if (lane < C::kCh) wmax[(warp & 3) * NR + c0 + lane] = mine;
-            }
-            named_bar_sync(bar_wg, 128);
-            if (tid < NR) {
-              const float m = fmaxf(fmaxf(wmax[tid], wmax[NR + tid]), fmaxf(wmax[2 * NR + tid], wmax[3 * NR + tid]));
-              const float was = ref[tid], now = fmaxf(fmaxf(was, m - C::kOff), kFloor);
-              ref[tid] = now;
-              shrink[tid] = fast_exp2(was - now);
-            }
-            named_bar_sync(bar_wg, 128);
-            if (!first) {
-#pragma unroll
-              for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-                uint32_t o[C::kCh];
-                tmem_get(o_col + c0, o);
-#pragma unroll
-                for (int c = 0; c < C::kCh; ++c) {
-                  const float f = shrink[c0 + c];
-                  o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                  l[c0 + c] *= f;
-                }
-                tmem_put(o_col + c0, o);
-              }
-              tmem_wait_st();
-            }
-            named_bar_sync(bar_wg, 128);  // the scratch is the P buffer
-          } else {
-            mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 125);  // P is free
-          }
-          // the weights, to shared memory as the B operand: [NR / 16 bytes][128 keys][16 bytes]
-#pragma unroll
-          for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-            if (C::kCh < NR) tmem_get(s_col + c0, s);
-            constexpr int kStep = F8 ? 16 : 8;
-#pragma unroll
-            for (int g = 0; g < C::kCh; g += kStep) {
-              uint32_t out[C::kPParts][4];
-#pragma unroll
-              for (int c = 0; c < kStep; c += 2) {
-                const int r = c0 + g + c;
-                const float p0 = fast_exp2(y_of(c0, g + c) - ref[r]), p1 = fast_exp2(y_of(c0, g + c + 1) - ref[r + 1]);
-                if constexpr (F8) {
-                  l[r] = fmaf(p0, inv, l[r]);
-                  l[r + 1] = fmaf(p1, inv, l[r + 1]);
-                  __half2 h = __floats2half2_rn(p0, p1);  // e5m2 is the upper byte of a half
-#pragma unroll
-                  for (int q = 0; q < 3; ++q) {
-                    const uint32_t e =
-                        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E5M2);
-                    if (c & 2) out[q][c / 4] |= e << 16;
-                    else out[q][c / 4] = e;
-                    const uint32_t wide = __byte_perm(e, 0, 0x1404);
-                    h = __hsub2(h, *reinterpret_cast<const __half2*>(&wide));
+                    for (int q = 0; q < 3; ++q) {
+                      const uint32_t e =
+                          __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E5M2);
+                      if (c & 2) out[q][c / 4] |= e << 16;
+                      else out[q][c / 4] = e;
+                      const uint32_t wide = __byte_perm(e, 0, 0x1404);
+                      h = __hsub2(h, *reinterpret_cast<const __half2*>(&wide));
+                    }
+                  } else {
+                    l[r / 2] = f32x2_add(l[r / 2], f32x2_pack(p0, p1));
+                    out[0][c / 2] = pack_bf16x2(p0, p1);
                   }
-                } else {
-                  l[r] += p0;
-                  l[r + 1] += p1;
-                  out[0][c / 2] = pack_bf16x2(p0, p1);
                 }
-              }
 #pragma unroll
-              for (int q = 0; q < C::kPParts; ++q)
-                *reinterpret_cast<uint4*>(pbuf + q * C::kPPart + (c0 + g) / kStep * 2048 + tid * 16) =
-                    make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
+                for (int q = 0; q < C::kPParts; ++q)
+                  *reinterpret_cast<uint4*>(pbuf + q * C::kPPart + (c0 + g) / kStep * 2048 + tid * 16) =
+                      make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
+              }
             }
+            // the first tile's references are the largest scores themselves
+            if (first || pass == 1 || bar_and(bar_wg, 128, !(top > C::kTop))) break;
+            move = true;
           }
-          if (kMask && !in) {
+          if (decltype(masked)::value && !in) {
             // what lies behind the sequence's end may be anything: zero weight
             // needs a finite value
             const int st = it % C::kVStages;
@@ -655,78 +723,68 @@ __global__ void __launch_bounds__(320, 1)
       }
 
       // ---- the segment's end: sums over the keys, the two warpgroups joined
-      const bool some = !first;
-      if (some) {
+      if (!first) {
         mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 127);
-        tc_fence_after();
+        constexpr int kSum = NR < 32 ? 16 : 32;
 #pragma unroll
-        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-          float v[C::kCh];
+        for (int c0 = 0; c0 < NR; c0 += kSum) {
+          float v[kSum];
 #pragma unroll
-          for (int c = 0; c < C::kCh; ++c) v[c] = l[c0 + c];
-          const float t = lane_totals<C::kCh>(v);
-          if (C::kCh == 32) lsum[(wg * 4 + (warp & 3)) * NR + c0 + lane] = t;
-          else if ((lane & 1) == 0) lsum[(wg * 4 + (warp & 3)) * NR + lane / 2] = t;
+          for (int c = 0; c < kSum; c += 2) f32x2_unpack(l[(c0 + c) / 2], v[c], v[c + 1]);
+          const float t = lane_totals<kSum>(v);
+          if (kSum == 32 || (lane & 1) == 0) lsum[(wg * 4 + (warp & 3)) * NR + c0 + (kSum == 32 ? lane : lane / 2)] = t;
         }
+      }
+      tc_fence_before();
+      named_bar_sync(bar_both, 256);
+      tc_fence_after();
+      const bool has0 = n > 1 || ((it - 1) & 1) == 0, has1 = n > 1 || ((it - 1) & 1) == 1;
+      const bool whole = w.t0 == 0 && w.t1 == w.nt;  // all of the sequence's tiles
+      // a partial segment's sums go to the block's first or second place
+      float* part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * NR * (D + 2);
+#pragma unroll 1
+      for (int r = threadIdx.x; r < rows; r += 256) {
+        const float m0 = has0 ? -nref_all[r] : -INFINITY, m1 = has1 ? -nref_all[NR + r] : -INFINITY;
+        const float M = fmaxf(m0, m1);
+        float f0 = 0.f, f1 = 0.f, L = 0.f;
+        if (has0) {
+          f0 = fast_exp2(m0 - M);
+          L += ((lsum[r] + lsum[NR + r]) + (lsum[2 * NR + r] + lsum[3 * NR + r])) * f0;
+        }
+        if (has1) {
+          f1 = fast_exp2(m1 - M);
+          L += ((lsum[4 * NR + r] + lsum[5 * NR + r]) + (lsum[6 * NR + r] + lsum[7 * NR + r])) * f1;
+        }
+        if (whole) {
+          const float by = L == 0.f ? 0.f : 1.f / L;  // a row that saw nothing: 0, -infinity
+          f0 *= by;
+          f1 *= by;
+          if (p.lse) p.lse[qb + row_at[r]] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        } else {
+          part[r * (D + 2) + D] = M;
+          part[r * (D + 2) + D + 1] = L;
+        }
+        weight[r] = f0;
+        weight[NR + r] = f1;
       }
       named_bar_sync(bar_both, 256);
-      const bool has0 = n > 1 || ((it - 1) & 1) == 0, has1 = n > 1 || ((it - 1) & 1) == 1;
-      auto part_of = [&](int v, int r, float M) { return fast_exp2(ref_all[v * NR + r] - M); };
-      auto top_of = [&](int r) {
-        return fmaxf(has0 ? ref_all[r] : -INFINITY, has1 ? ref_all[NR + r] : -INFINITY);
-      };
-      if (wg == 1 && has1 && has0) {
+      // lane = element of the value; the warpgroups take half of the rows each
+#pragma unroll 1
+      for (int c0 = wg * (NR / 2); c0 < min(rows, (wg + 1) * (NR / 2)); c0 += 8) {
+        uint32_t a[8], b[8];
+        tmem_ld(lanes + 2 * NR + c0, a);
+        tmem_ld(lanes + 3 * NR + c0, b);
+        tmem_landed(a);
+        tmem_landed(b);
+        if (tid < D) {
 #pragma unroll
-        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-          uint32_t o[C::kCh];
-          tmem_get(o_col + c0, o);
-#pragma unroll
-          for (int c = 0; c < C::kCh; ++c) {
+          for (int c = 0; c < 8; ++c) {
             const int r = c0 + c;
-            stage[r * 128 + tid] = __uint_as_float(o[c]) * part_of(1, r, top_of(r));
-          }
-        }
-      }
-      if (has0 && has1) named_bar_sync(bar_both, 256);
-      if (wg == (has0 ? 0 : 1)) {
-        // whole: the segment covers all of the sequence's tiles
-        const bool whole = w.t0 == 0 && w.t1 == w.nt;
-        // where a partial segment's sums go: the block's first or second place
-        const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-        float* part = p.part + slot * NR * (D + 2);
-#pragma unroll
-        for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-          uint32_t o[C::kCh];
-          tmem_get(o_col + c0, o);
-#pragma unroll
-          for (int c = 0; c < C::kCh; ++c) {
-            const int r = c0 + c;
-            if (r >= rows) continue;
-            const float M = top_of(r);
-            float a = __uint_as_float(o[c]), L = 0.f;
-            if (has0) {
-              const float f = part_of(0, r, M);
-              L += ((lsum[r] + lsum[NR + r]) + (lsum[2 * NR + r] + lsum[3 * NR + r])) * f;
-              a *= f;
-            }
-            if (has1) {
-              const float f = part_of(1, r, M);
-              L += ((lsum[4 * NR + r] + lsum[5 * NR + r]) + (lsum[6 * NR + r] + lsum[7 * NR + r])) * f;
-              if (has0) a += stage[r * 128 + tid];
-              else a *= f;
-            }
-            if (whole) {
-              const long long row = qb + row_at[r];
-              if (tid < D) p.o[row * D + tid] = __float2bfloat16(L == 0.f ? 0.f : a / L);
-              if (tid == 0 && p.lse)
-                p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-            } else {
-              if (tid < D) part[r * (D + 2) + tid] = a;
-              if (tid == 0) {
-                part[r * (D + 2) + D] = M;
-                part[r * (D + 2) + D + 1] = L;
-              }
-            }
+            if (r >= rows) break;
+            const float x = (has0 ? __uint_as_float(a[c]) * weight[r] : 0.f) +
+                            (has1 ? __uint_as_float(b[c]) * weight[NR + r] : 0.f);
+            if (whole) p.o[(qb + row_at[r]) * D + tid] = __float2bfloat16(x);
+            else part[r * (D + 2) + tid] = x;
           }
         }
       }
@@ -742,38 +800,62 @@ __global__ void __launch_bounds__(320, 1)
   }
 }
 
-// Joins the parts of the segments that several blocks shared, in the order of
-// their tiles: one block of D threads per row.
+// Joins the parts of the segments that several blocks shared: one block per row,
+// in 256 / D groups of threads that take every so manieth part, then added in
+// order.
 template <int D>
-__global__ void __launch_bounds__(D) tree_join_kernel(const TreeParams p, int nr) {
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int nr) {
+  constexpr int G = 256 / D;
+  __shared__ float wt[kMaxBlocks], acc[G][D], red[8];
   const int bh = blockIdx.y, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
   const int rg = blockIdx.x / nr, r = blockIdx.x % nr;  // nr rows of each row group
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ctx;
   const int nd = new_tokens(p, b, ctx), nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
   long long before, total;
   warp_prefix(p, b, before, total);
   const long long per = run_length(p, total), s0 = before + (long long)h * nt, s1 = s0 + nt;
-  const int first = (int)(s0 / per), last = (int)((s1 - 1) / per);
+  const int first = (int)(s0 / per), n = (int)((s1 - 1) / per) - first + 1;
   wait_prerequisite();  // every block: the launches that follow rely on this one being over last
-  if (rg * nr + r >= nd * p.group || first >= last) return;
-  float M = -INFINITY;
+  if (rg * nr + r >= nd * p.group || n <= 1) return;
   auto part_of = [&](int i) {
-    const long long slot = 2ll * (i * p.groups + rg) + (i == first ? 1 : 0);
+    const long long slot = 2ll * ((first + i) * p.groups + rg) + (i == 0 ? 1 : 0);
     return p.part + (slot * p.rows + r) * (D + 2);
   };
-  for (int i = first; i <= last; ++i) M = fmaxf(M, part_of(i)[D]);
-  float L = 0.f, a = 0.f;
-#pragma unroll 8
-  for (int i = first; i <= last; ++i) {
-    const float* x = part_of(i);
-    const float f = fast_exp2(x[D] - M);
-    L = fmaf(x[D + 1], f, L);
-    a = fmaf(x[threadIdx.x], f, a);
+  float m = -INFINITY, l = 0.f;
+  if (threadIdx.x < n) {
+    m = part_of(threadIdx.x)[D];
+    l = part_of(threadIdx.x)[D + 1];
   }
+  const float wm = warp_max(m);
+  if (lane == 0) red[warp] = wm;
+  __syncthreads();
+  float M = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) M = fmaxf(M, red[i]);
+  const float f = threadIdx.x < n ? fast_exp2(m - M) : 0.f;
+  if (threadIdx.x < n) wt[threadIdx.x] = f;
+  float L = threadIdx.x < n ? l * f : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+  __syncthreads();
+  if (lane == 0) red[warp] = L;
+  const int g = threadIdx.x / D, e = threadIdx.x % D;
+  float a = 0.f;
+#pragma unroll 8
+  for (int i = g; i < n; i += G) a = fmaf(part_of(i)[e], wt[i], a);
+  acc[g][e] = a;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int i = 1; i < G; ++i) a += acc[i][e];
+  L = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) L += red[i];
   const int t = (rg * nr + r) / p.group, hq = (rg * nr + r) % p.group;
   const long long row = ((long long)b * p.Hq + h * p.group + hq) * p.T + t;
-  p.o[row * D + threadIdx.x] = __float2bfloat16(L == 0.f ? 0.f : a / L);
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  p.o[row * D + e] = __float2bfloat16(L == 0.f ? 0.f : a / L);
+  if (e == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 int rows_per_block(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
@@ -796,7 +878,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, c
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.groups * std::min<long long>(NR, rows)), (unsigned)bh);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
