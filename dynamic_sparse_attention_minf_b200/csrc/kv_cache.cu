@@ -83,37 +83,37 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& q, uint32_t exp_byte) 
 }
 
 // One row of K and one of V per group of D / 8 lanes, kUnroll of them in
-// flight; rows run over (batch, head, token), tokens fastest.
+// flight; a block takes kRows * kUnroll tokens of one head.
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p) {
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p, int chunks) {
   constexpr int L = D / 8;
   constexpr int kRows = kThreads / L;
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
-  const int items = p.B * p.c.Hkv * p.N;
-  const int i0 = blockIdx.x * (kRows * kUnroll) + grp;
+  const int bh = blockIdx.x / chunks, h = bh % p.c.Hkv, b = bh / p.c.Hkv;
+  const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
+  int count = p.count ? __ldg(p.count + b) : p.N;
+  if (count < 0 || count > p.N) {
+    if (threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 100);
+    count = 0;
+  }
+  const int start = __ldg(p.start + b);
+  const __nv_bfloat16* kb = p.k + b * p.ksb + h * p.ksh + lane * 8;
+  const __nv_bfloat16* vb = p.v + b * p.vsb + h * p.vsh + lane * 8;
   uint4 rk[kUnroll], rv[kUnroll];
   long long dst[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long long i = (long long)i0 + u * kRows;
+    const int n = n0 + u * kRows;
     dst[u] = -1;
     rk[u] = rv[u] = make_uint4(0, 0, 0, 0);
-    if (i < items) {
-      const int n = (int)(i % p.N), bh = (int)(i / p.N);
-      const int h = bh % p.c.Hkv, b = bh / p.c.Hkv;
-      const int count = p.count ? __ldg(p.count + b) : p.N;
-      if (count < 0 || count > p.N) {
-        if (n == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 100);
-      } else if (n < count) {
-        const int src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
-        if (src < 0 || src >= p.M) {
-          report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
-        } else {
-          const int start = __ldg(p.start + b);
-          dst[u] = pool_row(p.c, b, h, start < 0 ? -1ll : (long long)start + n, p.status, 102);
-          rk[u] = __ldg(reinterpret_cast<const uint4*>(p.k + b * p.ksb + h * p.ksh + src * p.ksn) + lane);
-          rv[u] = __ldg(reinterpret_cast<const uint4*>(p.v + b * p.vsb + h * p.vsh + src * p.vsn) + lane);
-        }
+    if (n < count) {
+      const int src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
+      if (src < 0 || src >= p.M) {
+        report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
+      } else {
+        dst[u] = pool_row(p.c, b, h, start < 0 ? -1ll : (long long)start + n, p.status, 102);
+        rk[u] = __ldg(reinterpret_cast<const uint4*>(kb + src * p.ksn));
+        rv[u] = __ldg(reinterpret_cast<const uint4*>(vb + src * p.vsn));
       }
     }
   }
@@ -138,41 +138,38 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p) {
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p, int chunks) {
   constexpr int L = D / 8;
   constexpr int kRows = kThreads / L;
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
-  const int items = p.B * p.c.Hkv * p.N;
-  const int i0 = blockIdx.x * (kRows * kUnroll) + grp;
+  const int bh = blockIdx.x / chunks, h = bh % p.c.Hkv, b = bh / p.c.Hkv;
+  const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
   using Raw = typename std::conditional<F8, uint2, uint4>::type;
+  const int len = min(__ldg(p.lens + b), p.N);
   Raw rk[kUnroll], rv[kUnroll];
   uint32_t ek[kUnroll], ev[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long long i = (long long)i0 + u * kRows;
+    const int n = n0 + u * kRows;
     rk[u] = rv[u] = Raw{};
     ek[u] = ev[u] = 127;
-    if (i < items) {
-      const int n = (int)(i % p.N), bh = (int)(i / p.N);
-      const int h = bh % p.c.Hkv, b = bh / p.c.Hkv;
-      if (n < __ldg(p.lens + b)) {
-        const long long row = pool_row(p.c, b, h, n, p.status, 104);
-        if (row >= 0) {
-          constexpr int kEl = F8 ? 1 : 2;
-          rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
-          rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
-          if constexpr (F8) {
-            ek[u] = __ldg(p.c.ke + row);
-            ev[u] = __ldg(p.c.ve + row);
-          }
+    if (n < len) {
+      const long long row = pool_row(p.c, b, h, n, p.status, 104);
+      if (row >= 0) {
+        constexpr int kEl = F8 ? 1 : 2;
+        rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
+        rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
+        if constexpr (F8) {
+          ek[u] = __ldg(p.c.ke + row);
+          ev[u] = __ldg(p.c.ve + row);
         }
       }
     }
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long long i = (long long)i0 + u * kRows;
-    if (i >= items) continue;
+    const int n = n0 + u * kRows;
+    if (n >= p.N) continue;
     uint4 ok, ov;
     if constexpr (F8) {
       ok = dequantise8(rk[u], ek[u]);
@@ -181,39 +178,46 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
       ok = rk[u];
       ov = rv[u];
     }
-    reinterpret_cast<uint4*>(p.k + i * D)[lane] = ok;
-    reinterpret_cast<uint4*>(p.v + i * D)[lane] = ov;
+    const long long row = (long long)bh * p.N + n;
+    reinterpret_cast<uint4*>(p.k + row * D)[lane] = ok;
+    reinterpret_cast<uint4*>(p.v + row * D)[lane] = ov;
   }
 }
 
+// chunks of a head's N rows
 template <int D>
-int blocks_for(long long items) {
+int chunks_of(int N) {
   const int per = kThreads / (D / 8) * kUnroll;
-  return (int)((items + per - 1) / per);
+  return (N + per - 1) / per;
+}
+
+template <int D, bool F8>
+cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
+  const int chunks = chunks_of<D>(p.N);
+  kv_write_kernel<D, F8><<<(unsigned)(p.B * p.c.Hkv * chunks), kThreads, 0, stream>>>(p, chunks);
+  return cudaGetLastError();
+}
+template <int D, bool F8>
+cudaError_t launch_read(const KvReadParams& p, cudaStream_t stream) {
+  const int chunks = chunks_of<D>(p.N);
+  kv_read_kernel<D, F8><<<(unsigned)(p.B * p.c.Hkv * chunks), kThreads, 0, stream>>>(p, chunks);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t kv_write_launch(int d, const KvWriteParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.B * p.c.Hkv * p.N;
-  if (items == 0) return cudaSuccess;
-  if (d == 128 && p.c.ke) kv_write_kernel<128, true><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
-  else if (d == 128) kv_write_kernel<128, false><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
-  else if (d == 64 && p.c.ke) kv_write_kernel<64, true><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
-  else if (d == 64) kv_write_kernel<64, false><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
-  else return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (p.N == 0) return cudaSuccess;
+  if (d == 128) return p.c.ke ? launch_write<128, true>(p, stream) : launch_write<128, false>(p, stream);
+  if (d == 64) return p.c.ke ? launch_write<64, true>(p, stream) : launch_write<64, false>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t kv_read_launch(int d, const KvReadParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.B * p.c.Hkv * p.N;
-  if (items == 0) return cudaSuccess;
-  if (d == 128 && p.c.ke) kv_read_kernel<128, true><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
-  else if (d == 128) kv_read_kernel<128, false><<<blocks_for<128>(items), kThreads, 0, stream>>>(p);
-  else if (d == 64 && p.c.ke) kv_read_kernel<64, true><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
-  else if (d == 64) kv_read_kernel<64, false><<<blocks_for<64>(items), kThreads, 0, stream>>>(p);
-  else return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (p.N == 0) return cudaSuccess;
+  if (d == 128) return p.c.ke ? launch_read<128, true>(p, stream) : launch_read<128, false>(p, stream);
+  if (d == 64) return p.c.ke ? launch_read<64, true>(p, stream) : launch_read<64, false>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace minf

@@ -455,6 +455,7 @@ def minf_selftest_exp2(x, stream=None):
 # device, on that device's current stream unless `stream` says otherwise, and
 # allocates missing outputs there.
 E4M3 = torch.float8_e4m3fn
+_BF16, _I32, _I64, _F32, _F64 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float64
 
 
 def _need(ok, what):
@@ -462,17 +463,17 @@ def _need(ok, what):
         raise MinfError(what, 1)
 
 
-def _ints(fn, name, t, shape, device, dtype=torch.int32):
-    """An index tensor of the given shape on `device`."""
-    if not (t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
+def _same(fn, name, t, shape, device, dtype=_I32):
+    """Refuses a tensor that is not dense, of this shape and type, on `device`."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
         raise MinfError(f"{fn} ({name}: contiguous {dtype} {list(shape)} on {device})", 1)
 
 
-def _dense(fn, name, t, shape, device, dtype=torch.bfloat16):
-    """A dense tensor of the given shape on `device`, or a new one."""
+def _dense(fn, name, t, like, shape, dtype=_BF16):
+    """A dense tensor of the given shape on `like`'s device, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _ints(fn, name, t, shape, device, dtype)
+        return like.new_empty(shape, dtype=dtype)
+    _same(fn, name, t, shape, like.device, dtype)
     return t
 
 
@@ -480,27 +481,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """Makes a tensor's device and the call's stream current while the call's
-    outputs are allocated and its kernels launched."""
+def _ws(fn, ws, make, *args):
+    """The caller's workspace, or a new one."""
+    if ws is None:
+        return make(*args)
+    if not (ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == args[-1]):
+        raise MinfError(f"{fn} (ws: contiguous uint8 on {args[-1]})", 1)
+    return ws
 
-    def __init__(self, t, stream):
-        _need(t.is_cuda, "serving call (tensors in device memory)")
-        self.idx, self.stream = t.device.index, stream
 
-    def __enter__(self):
-        self.ctx = None
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.idx != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.idx)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _launch(t, stream, call):
+    """call(raw stream) with t's device and the call's stream current, so that
+    outputs are allocated where they are written."""
+    _need(t.is_cuda, "serving call (tensors in device memory)")
+    dev = t.get_device()
+    if stream is None:
+        if dev == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(dev))
+        with torch.cuda.device(dev):
+            return call(torch._C._cuda_getCurrentRawStream(dev))
+    _need(stream.device_index == dev, "serving call (stream of the tensors' device)")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def status_workspace(device="cuda"):
@@ -552,59 +554,75 @@ def minf_qkv_norm_rope(qkv, Hq, Hkv, pos=None, inv_freq=None, q_weight=None, k_w
     q [B, Hq, N, d], k and v [B, Hkv, N, d] (v is None without `want_v`), with the heads' norm and rotation
     (see include/minf.h).  pos [B, N] int32, inv_freq [rot_dim / 2] float64, weights [d] bf16."""
     fn = "minf_qkv_norm_rope"
-    _need(qkv.dtype == torch.bfloat16 and qkv.dim() == 3 and Hq > 0 and Hkv > 0 and
-          qkv.shape[2] % (Hq + 2 * Hkv) == 0 and qkv.stride(2) == 1, f"{fn} (qkv: bf16 [B, N, (Hq + 2 Hkv) * d])")
+    _need(qkv.dtype is _BF16 and qkv.dim() == 3 and Hq > 0 and Hkv > 0 and qkv.shape[2] % (Hq + 2 * Hkv) == 0
+          and (qkv.stride(2) == 1 or qkv.shape[2] == 1), f"{fn} (qkv: bf16 [B, N, (Hq + 2 Hkv) * d])")
     B, N, C = qkv.shape
-    d, dev = C // (Hq + 2 * Hkv), qkv.device
-    rot = 0
+    sb, sn, _ = qkv.stride()
+    d, dev, rot = C // (Hq + 2 * Hkv), qkv.device, 0
     if pos is not None:
-        _ints(fn, "pos", pos, (B, N), dev)
+        _same(fn, "pos", pos, (B, N), dev)
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _ints(fn, "inv_freq", inv_freq, (rot // 2,), dev, torch.float64)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _ints(fn, name, w, (d,), dev, torch.bfloat16)
-    with _On(qkv, stream) as st:
-        q = _dense(fn, "q", q, (B, Hq, N, d), dev)
-        k = _dense(fn, "k", k, (B, Hkv, N, d), dev)
-        v = _dense(fn, "v", v, (B, Hkv, N, d), dev) if want_v or v is not None else None
-        row = qkv.stride(1) if N > 1 else max(C, qkv.stride(1))
+        _same(fn, "inv_freq", inv_freq, (rot // 2,), dev, _F64)
+    if q_weight is not None:
+        _same(fn, "q_weight", q_weight, (d,), dev, _BF16)
+    if k_weight is not None:
+        _same(fn, "k_weight", k_weight, (d,), dev, _BF16)
+
+    def call(st):
+        oq = _dense(fn, "q", q, qkv, (B, Hq, N, d))
+        ok = _dense(fn, "k", k, qkv, (B, Hkv, N, d))
+        ov = _dense(fn, "v", v, qkv, (B, Hkv, N, d)) if want_v or v is not None else None
         _check(fn, lib().minf_qkv_norm_rope(
-            _ptr(qkv), B, N, Hq, Hkv, d, qkv.stride(0) if B > 1 else 0, row, _ptr(pos), _ptr(inv_freq), rot,
-            int(interleaved), _ptr(q_weight), _ptr(k_weight), eps, _ptr(q), _ptr(k), _ptr(v), st))
-    return q, k, v
+            qkv.data_ptr(), B, N, Hq, Hkv, d, sb if B > 1 else 0, sn if N > 1 else C, _ptr(pos),
+            _ptr(inv_freq), rot, 1 if interleaved else 0, _ptr(q_weight), _ptr(k_weight), eps, oq.data_ptr(),
+            ok.data_ptr(), _ptr(ov), st))
+        return oq, ok, ov
+
+    return _launch(qkv, stream, call)
 
 
 def _table(fn, cache, pages, B):
     _need(pages.dim() == 2, f"{fn} (pages: [B, max_pages])")
-    _ints(fn, "pages", pages, (B, pages.shape[1]), cache.device)
-    return pages.shape[1]
+    mp = pages.shape[1]
+    _same(fn, "pages", pages, (B, mp), cache.device)
+    return mp
+
+
+def _strides(t):
+    """Batch, head and row strides; those of a single one do not matter."""
+    return _Strides(*(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride())))
+
+
+_Strides = ctypes.c_int64 * 3
 
 
 def minf_kv_write(k, v, cache: KVCache, pages, start, count=None, rows=None, ws=None, stream=None):
     """Writes k, v [B, Hkv, M, d] (d contiguous, other strides multiples of 8) into the cache at positions
     start[b] + i, i < count[b] (see include/minf.h); with `rows` [B, N] position start[b] + i gets row rows[b, i]."""
     fn = "minf_kv_write"
-    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.bfloat16 and
-          k.device == v.device == cache.device and k.shape[1] == cache.Hkv and k.shape[3] == cache.d and
-          k.stride(3) == v.stride(3) == 1, f"{fn} (k, v: bf16 [B, Hkv, M, d] of the cache's Hkv, d and device)")
+    dev = cache.device
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype is _BF16 and v.dtype is _BF16 and k.device == dev
+          and v.device == dev and k.shape[1] == cache.Hkv and k.shape[3] == cache.d and k.stride(3) == 1
+          and v.stride(3) == 1, f"{fn} (k, v: bf16 [B, Hkv, M, d] of the cache's Hkv, d and device)")
     B, _, M, _ = k.shape
-    mp, dev = _table(fn, cache, pages, B), cache.device
-    _ints(fn, "start", start, (B,), dev)
+    mp = _table(fn, cache, pages, B)
+    _same(fn, "start", start, (B,), dev)
     if count is not None:
-        _ints(fn, "count", count, (B,), dev)
+        _same(fn, "count", count, (B,), dev)
     N = M
     if rows is not None:
         _need(rows.dim() == 2, f"{fn} (rows: [B, N])")
         N = rows.shape[1]
-        _ints(fn, "rows", rows, (B, N), dev)
-    strides = [(ctypes.c_int64 * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))) for t in (k, v)]
-    with _On(k, stream) as st:
-        if ws is None:
-            ws = status_workspace(dev)
-        _check(fn, lib().minf_kv_write(cache._ref, _ptr(k), _ptr(v), B, N, M, strides[0], strides[1], _ptr(pages), mp,
-                                       _ptr(start), _ptr(count), _ptr(rows), _ptr(ws), ws.numel(), st))
+        _same(fn, "rows", rows, (B, N), dev)
+
+    def call(st):
+        w = _ws(fn, ws, status_workspace, dev)
+        _check(fn, lib().minf_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), B, N, M, _strides(k), _strides(v),
+                                       pages.data_ptr(), mp, start.data_ptr(), _ptr(count), _ptr(rows), w.data_ptr(),
+                                       w.numel(), st))
+
+    _launch(k, stream, call)
 
 
 def minf_kv_read(cache: KVCache, pages, lens, N, k=None, v=None, ws=None, stream=None):
@@ -613,15 +631,17 @@ def minf_kv_read(cache: KVCache, pages, lens, N, k=None, v=None, ws=None, stream
     _need(pages.dim() == 2 and N >= 0, f"{fn} (pages: [B, max_pages], N >= 0)")
     B, dev = pages.shape[0], cache.device
     mp = _table(fn, cache, pages, B)
-    _ints(fn, "lens", lens, (B,), dev)
-    with _On(cache.k, stream) as st:
-        k = _dense(fn, "k", k, (B, cache.Hkv, N, cache.d), dev)
-        v = _dense(fn, "v", v, (B, cache.Hkv, N, cache.d), dev)
-        if ws is None:
-            ws = status_workspace(dev)
-        _check(fn, lib().minf_kv_read(cache._ref, _ptr(pages), B, mp, _ptr(lens), N, _ptr(k), _ptr(v), _ptr(ws),
-                                      ws.numel(), st))
-    return k, v
+    _same(fn, "lens", lens, (B,), dev)
+
+    def call(st):
+        ok = _dense(fn, "k", k, cache.k, (B, cache.Hkv, N, cache.d))
+        ov = _dense(fn, "v", v, cache.k, (B, cache.Hkv, N, cache.d))
+        w = _ws(fn, ws, status_workspace, dev)
+        _check(fn, lib().minf_kv_read(cache._ref, pages.data_ptr(), B, mp, lens.data_ptr(), N, ok.data_ptr(),
+                                      ov.data_ptr(), w.data_ptr(), w.numel(), st))
+        return ok, ov
+
+    return _launch(cache.k, stream, call)
 
 
 def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=None, o=None, lse=None, want_lse=True,
@@ -631,21 +651,24 @@ def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=N
     token u; None is a chain.  n_draft [B] int32: tokens of each sequence (None: T); rows behind them are not
     written (a new `o` is not initialised there)."""
     fn = "minf_tree_attn"
-    _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.device == cache.device and
-          q.shape[3] == cache.d, f"{fn} (q: contiguous bf16 [B, Hq, T, d] of the cache's d and device)")
+    dev = cache.device
+    _need(q.dim() == 4 and q.dtype is _BF16 and q.is_contiguous() and q.device == dev and q.shape[3] == cache.d,
+          f"{fn} (q: contiguous bf16 [B, Hq, T, d] of the cache's d and device)")
     B, Hq, T, d = q.shape
-    mp, dev = _table(fn, cache, pages, B), cache.device
-    _ints(fn, "ctx_lens", ctx_lens, (B,), dev)
+    mp = _table(fn, cache, pages, B)
+    _same(fn, "ctx_lens", ctx_lens, (B,), dev)
     if n_draft is not None:
-        _ints(fn, "n_draft", n_draft, (B,), dev)
+        _same(fn, "n_draft", n_draft, (B,), dev)
     if tree_mask is not None:
-        _ints(fn, "tree_mask", tree_mask, (B, T), dev, torch.int64)
-    with _On(q, stream) as st:
-        o = _dense(fn, "o", o, (B, Hq, T, d), dev)
-        if want_lse or lse is not None:
-            lse = _dense(fn, "lse", lse, (B, Hq, T), dev, torch.float32)
-        if ws is None:
-            ws = tree_attn_workspace(B, Hq, cache.Hkv, T, d, dev)
-        _check(fn, lib().minf_tree_attn(cache._ref, _ptr(q), B, Hq, T, scale, _ptr(pages), mp, _ptr(ctx_lens),
-                                        _ptr(n_draft), _ptr(tree_mask), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), st))
-    return o, lse
+        _same(fn, "tree_mask", tree_mask, (B, T), dev, _I64)
+
+    def call(st):
+        oo = torch.empty_like(q) if o is None else _dense(fn, "o", o, q, (B, Hq, T, d))
+        ol = _dense(fn, "lse", lse, q, (B, Hq, T), _F32) if want_lse or lse is not None else None
+        w = _ws(fn, ws, tree_attn_workspace, B, Hq, cache.Hkv, T, d, dev)
+        _check(fn, lib().minf_tree_attn(cache._ref, q.data_ptr(), B, Hq, T, scale, pages.data_ptr(), mp,
+                                        ctx_lens.data_ptr(), _ptr(n_draft), _ptr(tree_mask), oo.data_ptr(), _ptr(ol),
+                                        w.data_ptr(), w.numel(), st))
+        return oo, ol
+
+    return _launch(q, stream, call)
