@@ -196,6 +196,7 @@ minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B
   if (!Q || !O || !ctx_lens || Hq < 1 || Hq % cache->Hkv != 0 || T < 1) return MINF_ERR_INVALID_ARG;
   if (T > 64 || !tree_rows_supported(Hq, cache->Hkv, T) || (long long)B * cache->Hkv > 65535)
     return MINF_ERR_UNSUPPORTED;
+  if (((long long)max_pages * cache->page + 127) / 128 * B * cache->Hkv >= (1ll << 30)) return MINF_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(O) || ((uintptr_t)tree_mask & 7)) return MINF_ERR_INVALID_ARG;
   if ((long long)B * Hq * T >= (1ll << 31)) return MINF_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, minf_tree_attn_workspace(B, Hq, cache->Hkv, T, cache->d))) != MINF_OK) return st;

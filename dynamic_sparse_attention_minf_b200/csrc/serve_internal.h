@@ -69,9 +69,9 @@ struct TreeParams {
   float scale_log2;
   float* part;             // workspace
   DevStatus* status;
-  // set by the launch: row groups of `rows` rows, and the number and least
-  // length of the runs that the tile list is cut into
-  int groups, rows, lanes, min_run;
+  // set by the launch: row groups of `rows` rows, and the number of runs that
+  // the tile list is cut into
+  int groups, rows, lanes;
 };
 size_t tree_part_floats(int Hq, int Hkv, int T, int d);
 bool tree_rows_supported(int Hq, int Hkv, int T);

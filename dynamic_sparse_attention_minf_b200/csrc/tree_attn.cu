@@ -61,45 +61,41 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
 }
 
 // Tiles before sequence b, and in all, of the warp's choice of b.
-__device__ __forceinline__ void warp_prefix(const TreeParams& p, int upto, long long& before, long long& total) {
+__device__ __forceinline__ void warp_prefix(const TreeParams& p, int upto, int& before, int& total) {
   const int lane = threadIdx.x & 31;
-  long long a = 0, t = 0;
+  int a = 0, t = 0;
   for (int b = lane; b < p.B; b += 32) {
     const int n = tiles_of(p, b);
     t += n;
     if (b < upto) a += n;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-  }
-  before = a * p.c.Hkv;
-  total = t * p.c.Hkv;
+  before = __reduce_add_sync(0xFFFFFFFFu, a) * p.c.Hkv;
+  total = __reduce_add_sync(0xFFFFFFFFu, t) * p.c.Hkv;
 }
-__device__ __forceinline__ long long run_length(const TreeParams& p, long long total) {
-  return max((long long)p.min_run, (total + p.lanes - 1) / p.lanes);
+// tiles of a block's run
+__device__ __forceinline__ int run_length(const TreeParams& p, int total) {
+  return max(1, (int)((unsigned)(total + p.lanes - 1) / (unsigned)p.lanes));
 }
 
 // A block's run [g, g1) of the tile list (sequence-major, then KV head, then
 // tile), walked one (sequence, head) segment at a time; every role of the block
 // walks it by itself.
 struct Walk {
-  long long g, g1, base;  // base: first tile of sequence b
-  int b, nt;              // nt: tiles per head of sequence b
+  int g, g1, base;  // base: first tile of sequence b
+  int b, nt;        // nt: tiles per head of sequence b
   // the current segment: tiles [t0, t1) of KV head h of sequence b
   int h, t0, t1, ctx, nd;
   __device__ __forceinline__ bool next(const TreeParams& p) {
     if (g >= g1) return false;
-    while (g >= base + (long long)nt * p.c.Hkv) {
-      base += (long long)nt * p.c.Hkv;
+    while (g >= base + nt * p.c.Hkv) {
+      base += nt * p.c.Hkv;
       ++b;
       nt = tiles_of(p, b);
     }
-    const long long x = g - base;
-    h = (int)(x / nt);
-    t0 = (int)(x % nt);
-    t1 = (int)min((long long)nt, t0 + (g1 - g));
+    const unsigned x = g - base;
+    h = x / (unsigned)nt;
+    t0 = x - h * nt;
+    t1 = min(nt, t0 + (g1 - g));
     nd = new_tokens(p, b, ctx);
     g += t1 - t0;
     return true;
@@ -109,7 +105,11 @@ struct Walk {
 // --------------------------------------------------------------------- layout
 template <int D, bool F8, int NR>
 struct Cfg {
-  static constexpr int kThreads = 320;                // two softmax warpgroups, issuer, producer
+  // softmax warpgroups, on alternate tiles: four where TMEM and registers allow
+  // (one tile's chain of waits is longer than its loads), two otherwise
+  static constexpr int kWG = NR <= 32 ? 4 : 2;
+  static constexpr int kSoft = 128 * kWG;
+  static constexpr int kThreads = kSoft + 96;         // and the issuer, the K and the V producer
   static constexpr int kRowB = D * (F8 ? 1 : 2);       // bytes of a cached row
   static constexpr int kPitch = kRowB < 128 ? kRowB : 128;  // row pitch within a swizzled region
   static constexpr int kRegions = kRowB / kPitch;
@@ -120,38 +120,38 @@ struct Cfg {
   static constexpr int kPPart = NR * 128 * (F8 ? 1 : 2);
   static constexpr int kQB = kQParts * kQPart;
   static constexpr int kPB = kPParts * kPPart;         // of one warpgroup
-  static constexpr int kMiscMax = 2 * NR * 4 + NR * 4 + (F8 ? NR * 4 : 0) + NR * 8 + 512;
+  static constexpr int kMiscMax = kWG * NR * 4 + NR * 4 + (F8 ? NR * 4 : 0) + NR * 8 + 512;
   static constexpr int kExpB = F8 ? 256 : 0;           // a tile's key and value exponents
-  static constexpr int kTiles = (232448 - kQB - 2 * kPB - kMiscMax - 8 * kExpB) / kTileB;
+  static constexpr int kTiles = (232448 - kQB - kWG * kPB - kMiscMax - 8 * kExpB) / kTileB;
   static constexpr int kKStages = (kTiles + 1) / 2 < 8 ? (kTiles + 1) / 2 : 8;
   static constexpr int kVStages = kTiles / 2 < 8 ? kTiles / 2 : 8;
   static constexpr int kOffV = 0;                      // the rings first: a 64-element V tile is read
   static constexpr int kOffK = kOffV + kVStages * kTileB;  // past its end by the unused 64 output rows
   static constexpr int kOffQ = kOffK + kKStages * kTileB;
   static constexpr int kOffP = kOffQ + kQB;
-  static constexpr int kOffExp = kOffP + 2 * kPB;
-  static constexpr int kOffRef = kOffExp + kKStages * kExpB;  // [2][NR] references
-  static constexpr int kOffRow = kOffRef + 2 * NR * 4;        // [NR] row of the KV head's [group, T] queries
+  static constexpr int kOffExp = kOffP + kWG * kPB;
+  static constexpr int kOffRef = kOffExp + kKStages * kExpB;  // [kWG][NR] references
+  static constexpr int kOffRow = kOffRef + kWG * NR * 4;      // [NR] row of the KV head's [group, T] queries
   static constexpr int kOffFac = kOffRow + NR * 4;            // [NR] row factors (8-bit)
   static constexpr int kOffWords = kOffFac + (F8 ? NR * 4 : 0);  // [NR] mask words
   static constexpr int kOffBars = kOffWords + NR * 8;
-  // k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], pv_done[2], q_full, mma_done
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8;
+  // k_full, k_empty, v_full, v_empty, s_full, p_full, pv_done [kWG], q_full, mma_done
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kWG + 2;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;    // TMEM slot, abort, the run
   static constexpr int kSmem = kOffMisc + 48;
   static constexpr uint32_t kSwizzle = kPitch == 128 ? 2u : 4u;
   static constexpr uint32_t kGroup8 = 8 * kPitch;             // eight rows of a region
-  static constexpr int kTmem = 4 * NR;                        // S and O of two warpgroups
+  static constexpr int kTmem = 2 * kWG * NR;                  // S and O of the warpgroups
   static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, NR, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
   static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, NR, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
-  static constexpr int kCh = NR < 32 || NR == 128 ? 16 : 32;  // columns a thread takes at once
+  static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
   static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(24 * NR <= kPB && 40 * NR <= kQB, "scratch in the idle P and Q buffers");
-  static_assert(NR * D * 2 <= 2 * kPB, "the queries as they are in the idle P buffers");
+  static_assert(24 * NR <= kPB && 20 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
+  static_assert(NR * D * 2 <= kWG * kPB && kTmem >= 32, "the queries as they are in the idle P buffers");
 };
 
 // Sums each of N values (16 or 32) over the warp's lanes; lane i ends with the
@@ -179,7 +179,7 @@ __device__ __forceinline__ float lane_totals(float (&v)[N]) {
 }
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const TreeParams p) {
   using C = Cfg<D, F8, NR>;
@@ -191,9 +191,10 @@ __global__ void __launch_bounds__(320, 1)
   uint64_t* v_full = k_empty + C::kKStages;
   uint64_t* v_empty = v_full + C::kVStages;
   uint64_t* s_full = v_empty + C::kVStages;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* q_full = pv_done + 2;
+  uint64_t* p_full = s_full + C::kWG;
+  uint64_t* pv_done = p_full + C::kWG;
+  uint64_t* q_full = pv_done + C::kWG;
+  constexpr int kIssuer = 4 * C::kWG, kLoadK = kIssuer + 1, kLoadV = kIssuer + 2;  // warps
   uint64_t* mma_done = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -203,10 +204,10 @@ __global__ void __launch_bounds__(320, 1)
     if (threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 112);
     return;
   }
-  if (warp == 8) {
-    tmem_alloc(tmem_slot, C::kTmem < 32 ? 32 : C::kTmem);
+  if (warp == kIssuer) {
+    tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
-  } else if (warp == 9) {
+  } else if (warp == kLoadK) {
     if (lane == 0) {
       for (int s = 0; s < C::kKStages; ++s) {
         mbar_init(&k_full[s], 1);
@@ -216,12 +217,12 @@ __global__ void __launch_bounds__(320, 1)
         mbar_init(&v_full[s], 1);
         mbar_init(&v_empty[s], 1);
       }
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < C::kWG; ++w) {
         mbar_init(&s_full[w], 1);
         mbar_init(&p_full[w], 128);
         mbar_init(&pv_done[w], 1);
       }
-      mbar_init(q_full, 256);
+      mbar_init(q_full, C::kSoft);
       mbar_init(mma_done, 1);
       *abort = 0;
       fence_mbar_init();
@@ -230,9 +231,9 @@ __global__ void __launch_bounds__(320, 1)
     }
   } else if (warp == 0) {
     // this block's run of the tile list, and the sequence that it begins in
-    long long before, total;
+    int before, total;
     warp_prefix(p, 0, before, total);
-    const long long per = run_length(p, total);
+    const int per = run_length(p, total);
     Walk w;
     w.g = min(total, part_lane * per);
     w.g1 = min(total, w.g + per);
@@ -248,15 +249,15 @@ __global__ void __launch_bounds__(320, 1)
           const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
           if (lane >= o) incl += up;
         }
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + (long long)incl * p.c.Hkv > w.g);
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > w.g);
         if (past) {
           const int at = __ffs(past) - 1;
-          w.base += (long long)(__shfl_sync(0xFFFFFFFFu, incl, at) - __shfl_sync(0xFFFFFFFFu, n, at)) * p.c.Hkv;
+          w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - __shfl_sync(0xFFFFFFFFu, n, at)) * p.c.Hkv;
           w.b = b0 + at;
           w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
           break;
         }
-        w.base += (long long)__shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
+        w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
       }
     }
     if (lane == 0) *start = w;
@@ -275,35 +276,20 @@ __global__ void __launch_bounds__(320, 1)
   Walk w = *start;
   __syncthreads();  // the run's place is the P buffer
 
-  if (warp == 9) {
-    // ------------------------------------------------------------ producer
-    int nk = 0, nv = 0;
-    // One tile's pages: lane i < pages loads page i.  With K go, in 8 bits, the
-    // exponents of the tile's keys and values, four keys per lane.
-    auto load_tile = [&](bool is_k, int row0, int pages, uint32_t ke, uint32_t ve) {
-      const int n = is_k ? nk : nv, stages = is_k ? C::kKStages : C::kVStages;
-      const int st = n % stages;
-      uint64_t* full = (is_k ? k_full : v_full) + st;
-      if (n >= stages)
-        mbar_wait_or_abort((is_k ? k_empty : v_empty) + st, ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
-      if (__any_sync(0xFFFFFFFFu, *abort)) return;
-      if (F8 && is_k) {
-        uint32_t* e = reinterpret_cast<uint32_t*>(smem + C::kOffExp + st * C::kExpB) + lane;
-        e[0] = ke;
-        e[32] = ve;
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive_expect_tx(full, (pages << p.c.log_page) * C::kRowB);
-      __syncwarp();
-      uint8_t* dst = smem + (is_k ? C::kOffK : C::kOffV) + st * C::kTileB + (lane << p.c.log_page) * C::kPitch;
-      if (lane < pages) {
-#pragma unroll
-        for (int r = 0; r < C::kRegions; ++r)
-          tma_load_2d(dst + r * C::kRegion, is_k ? &tmK : &tmV, full, r * 64, row0);
-      }
-      __syncwarp();
-      (is_k ? nk : nv) = n + 1;
-    };
+  if (warp == kLoadK || warp == kLoadV) {
+    // ----------------------------------------------------------- producers
+    // One warp loads the K tiles and one the V tiles, each tile page by page
+    // (lane i < pages loads page i): a box costs its warp about 100 cycles to
+    // issue, and with pages of 16 rows a tile has 8 or 16 boxes of each.  With K
+    // go, in 8 bits, the exponents of the tile's keys and values, four keys per
+    // lane.  Page ids are read two tiles ahead, exponents one.
+    const bool is_k = warp == kLoadK;
+    const int stages = is_k ? C::kKStages : C::kVStages;
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    uint8_t* ring = smem + (is_k ? C::kOffK : C::kOffV);
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
+    int n = 0;
     // failure-detection test hook: the first block withholds its key tiles, so its
     // bounded waits run out and the call reports a timeout
     bool live = p.status->withhold == 0 || blockIdx.x != 0;
@@ -326,57 +312,67 @@ __global__ void __launch_bounds__(320, 1)
         const int pg = (4 * lane) >> p.c.log_page;
         const int at = __shfl_sync(0xFFFFFFFFu, row, pg) + ((4 * lane) & ((1 << p.c.log_page) - 1));
         ke = ve = 0;
-        if (F8 && pg < pages) {
+        if (pg < pages) {
           ke = __ldg(reinterpret_cast<const uint32_t*>(p.c.ke + at));
           ve = __ldg(reinterpret_cast<const uint32_t*>(p.c.ve + at));
         }
       };
-      // page ids are read two tiles ahead, exponents one; V trails K by one tile
-      int pages = 0, row = fetch(w.t0, pages), pages_n = 0, row_n = 0, pages_v = 0, row_v = 0;
-      uint32_t ke, ve, ke_n = 0, ve_n = 0;
+      int pages = 0, row = fetch(w.t0, pages), pages_n = 0, row_n = 0;
+      uint32_t ke = 0, ve = 0, ke_n = 0, ve_n = 0;
       if (w.t0 + 1 < w.t1) row_n = fetch(w.t0 + 1, pages_n);
-      exponents(row, pages, ke, ve);
-      for (int t = w.t0; t <= w.t1; ++t) {
+      if (F8 && is_k) exponents(row, pages, ke, ve);
+      for (int t = w.t0; t < w.t1; ++t, ++n) {
         int pages_2 = 0, row_2 = 0;
         if (t + 2 < w.t1) row_2 = fetch(t + 2, pages_2);
-        exponents(row_n, pages_n, ke_n, ve_n);
-        if (t < w.t1) load_tile(true, row, pages, ke, ve);
-        if (t > w.t0) load_tile(false, row_v, pages_v, 0, 0);
-        pages_v = pages;
-        row_v = row;
+        if (F8 && is_k) exponents(row_n, pages_n, ke_n, ve_n);
+        const int st = n % stages;
+        if (n >= stages)
+          mbar_wait_or_abort(&empty[st], ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
+        if (__any_sync(0xFFFFFFFFu, *abort)) {
+          live = false;
+          break;
+        }
+        if (F8 && is_k) {
+          uint32_t* e = reinterpret_cast<uint32_t*>(smem + C::kOffExp + st * C::kExpB) + lane;
+          e[0] = ke;
+          e[32] = ve;
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (pages << p.c.log_page) * C::kRowB);
+        __syncwarp();
+        if (lane < pages) {
+          uint8_t* dst = ring + st * C::kTileB + (lane << p.c.log_page) * C::kPitch;
+#pragma unroll
+          for (int r = 0; r < C::kRegions; ++r) tma_load_2d(dst + r * C::kRegion, map, &full[st], r * 64, row);
+        }
+        __syncwarp();
         pages = pages_n;
         row = row_n;
         pages_n = pages_2;
         row_n = row_2;
         ke = ke_n;
         ve = ve_n;
-        if (__any_sync(0xFFFFFFFFu, *abort)) {
-          live = false;
-          break;
-        }
       }
     }
     if (lane == 0) {  // never exit with copies in flight
       int dummy = 0;
-      for (int n = max(0, nk - C::kKStages); n < nk; ++n)
-        mbar_wait(&k_full[n % C::kKStages], (n / C::kKStages) & 1, &dummy, p.status, 115);
-      for (int n = max(0, nv - C::kVStages); n < nv; ++n)
-        mbar_wait(&v_full[n % C::kVStages], (n / C::kVStages) & 1, &dummy, p.status, 116);
+      for (int i = max(0, n - stages); i < n; ++i)
+        mbar_wait(&full[i % stages], (i / stages) & 1, &dummy, p.status, is_k ? 115 : 116);
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == kIssuer) {
     // --------------------------------------------------------- MMA issuer
     const uint32_t q0 = smem_u32(smem + C::kOffQ);
     int it = 0, segs = 0;
     // O^T of the tile's warpgroup (+)= V^T P
     auto issue_pv = [&](int i, bool first) {
-      const int wg = i & 1, st = i % C::kVStages;
-      mbar_wait_or_abort(&p_full[wg], (i >> 1) & 1, abort, p.status, 117);
+      const int wg = i % C::kWG, st = i % C::kVStages;
+      mbar_wait_or_abort(&p_full[wg], (i / C::kWG) & 1, abort, p.status, 117);
       mbar_wait_or_abort(&v_full[st], (i / C::kVStages) & 1, abort, p.status, 118);
       if (__any_sync(0xFFFFFFFFu, *abort)) return;
       tc_fence_after();
       const uint32_t v = smem_u32(smem + C::kOffV + st * C::kTileB), pb = smem_u32(smem + C::kOffP + wg * C::kPB);
-      const uint32_t d = tmem + 2 * NR + wg * NR;
+      const uint32_t d = tmem + (C::kWG + wg) * NR;
       if (elect_lane()) {
 #pragma unroll
         for (int part = 0; part < C::kPParts; ++part)
@@ -400,7 +396,7 @@ __global__ void __launch_bounds__(320, 1)
       ++segs;
       const int n = w.t1 - w.t0;
       for (int i = 0; i < n; ++i, ++it) {
-        const int wg = it & 1, st = it % C::kKStages;
+        const int wg = it % C::kWG, st = it % C::kKStages;
         mbar_wait_or_abort(&k_full[st], (it / C::kKStages) & 1, abort, p.status, 120);
         if (__any_sync(0xFFFFFFFFu, *abort)) break;
         tc_fence_after();
@@ -421,9 +417,13 @@ __global__ void __launch_bounds__(320, 1)
           umma_commit(&k_empty[st]);
         }
         __syncwarp();
-        if (i > 0) issue_pv(it - 1, i - 1 < 2);
+        // scores run ahead of the weights by one tile less than there are
+        // warpgroups: PV(it - kWG), before this, has waited for the tile whose S
+        // buffer this one takes
+        if (i >= C::kWG - 1) issue_pv(it - (C::kWG - 1), i - (C::kWG - 1) < C::kWG);
       }
-      if (!__any_sync(0xFFFFFFFFu, *abort)) issue_pv(it - 1, n - 1 < 2);
+      for (int i = max(0, n - (C::kWG - 1)); i < n && !__any_sync(0xFFFFFFFFu, *abort); ++i)
+        issue_pv(it - n + i, i < C::kWG);
     }
     if (elect_lane()) umma_commit(mma_done);
     __syncwarp();
@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(320, 1)
     // every later wait ends at once, and the barriers below keep their counts.
     const int wg = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_col = lanes + wg * NR, o_col = lanes + 2 * NR + wg * NR;
-    // the references, negated: [2][NR]
+    const uint32_t s_col = lanes + wg * NR, o_col = lanes + (C::kWG + wg) * NR;
+    // the references, negated: [kWG][NR]
     float* nref_all = reinterpret_cast<float*>(smem + C::kOffRef);
     float* nref = nref_all + wg * NR;
     float* fac = reinterpret_cast<float*>(smem + C::kOffFac);
@@ -450,9 +450,9 @@ __global__ void __launch_bounds__(320, 1)
     float* wmax = reinterpret_cast<float*>(pbuf);             // [4][NR] while P is idle
     float* shrink = wmax + 4 * NR;                            // [NR]
     float* nwas = shrink + NR;                                // [NR]
-    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ);  // [2][4][NR] while Q is idle
-    float* weight = lsum + 8 * NR;                            // [2][NR]
-    const int bar_wg = 1 + wg, bar_both = 3;
+    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ);  // [kWG][4][NR] while Q is idle
+    float* weight = lsum + C::kWG * 4 * NR;                   // [kWG][NR]
+    const int bar_wg = 1 + wg, bar_all = 1 + C::kWG;
     int it = 0, uses = 0;  // tiles of the block so far, and those of this warpgroup
     while (w.next(p)) {
       const int rows = min(NR, w.nd * p.group - rg * NR);
@@ -460,43 +460,43 @@ __global__ void __launch_bounds__(320, 1)
       const int len = w.ctx + w.nd, n = w.t1 - w.t0;
       const long long qb = ((long long)w.b * p.Hq + w.h * p.group) * p.T;  // first query row of the KV head
       // ---- the segment's queries, as the B operand; their mask words
-#pragma unroll 1
-      for (int r = threadIdx.x; r < NR; r += 256) {
-        unsigned long long m = 0;
-        if (r < rows) {
-          const int t = (rg * NR + r) / p.group, hq = (rg * NR + r) % p.group;
-          row_at[r] = hq * p.T + t;
-          m = p.mask ? p.mask[(long long)w.b * p.T + t] : (2ull << t) - 1;
-          if (w.nd < 64) m &= (1ull << w.nd) - 1;
-        }
-        words[r] = m;
-        nref_all[r] = nref_all[NR + r] = INFINITY;
-      }
-      named_bar_sync(bar_both, 256);
       {
-        // 16-byte pieces: bf16 queries go where the product reads them, 8-bit ones
-        // are staged in the P buffer (rows of D) and split below
-        constexpr int kPieces = NR * (D / 8) / 256 > 0 ? NR * (D / 8) / 256 : 1;
+        // 16-byte pieces, each thread's all of one row: bf16 queries go where the
+        // product reads them, 8-bit ones are staged in the P buffer (rows of D) and
+        // split below
+        constexpr int kStep = C::kSoft / NR, kPieces = (D / 8 + kStep - 1) / kStep;
+        const int r = threadIdx.x % NR, c0 = threadIdx.x / NR;
+        const int t = (unsigned)(rg * NR + r) / (unsigned)p.group, at = (rg * NR + r - t * p.group) * p.T + t;
         uint4 x[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int id = i * 256 + threadIdx.x, r = id % NR, c = id / NR;
+          const int c = c0 + i * kStep;
           x[i] = make_uint4(0, 0, 0, 0);
-          if (id < NR * (D / 8) && r < rows)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + row_at[r]) * D) + c);
+          if (c < D / 8 && r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + at) * D) + c);
+        }
+        if (c0 == 0) {
+          unsigned long long m = 0;
+          if (r < rows) {
+            m = p.mask ? p.mask[(long long)w.b * p.T + t] : (2ull << t) - 1;
+            if (w.nd < 64) m &= (1ull << w.nd) - 1;
+          }
+          row_at[r] = at;
+          words[r] = m;
+#pragma unroll
+          for (int v = 0; v < C::kWG; ++v) nref_all[v * NR + r] = INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int id = i * 256 + threadIdx.x, r = id % NR, c = id / NR;
-          if (id < NR * (D / 8))
+          const int c = c0 + i * kStep;
+          if (c < D / 8)
             *reinterpret_cast<uint4*>(smem + (F8 ? C::kOffP + r * D * 2 + c * 16 : C::kOffQ + c * NR * 16 + r * 16)) = x[i];
         }
       }
       if constexpr (F8) {
-        named_bar_sync(bar_both, 256);
+        named_bar_sync(bar_all, C::kSoft);
         constexpr int E = D / 32;
 #pragma unroll 1
-        for (int r = warp; r < NR; r += 8) {
+        for (int r = warp; r < NR; r += 4 * C::kWG) {
           float x[E];
           float top = 0.f;
           bool bad = false;
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(320, 1)
       }
       fence_proxy_async();
       mbar_arrive(q_full);
-      named_bar_sync(bar_both, 256);
+      named_bar_sync(bar_all, C::kSoft);
 
       uint64_t l[NR / 2];  // this key lane's sums of two rows each
 #pragma unroll
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(320, 1)
       bool first = true;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++it) {
-        if ((it & 1) != wg) continue;
+        if (it % C::kWG != wg) continue;
         const int j0 = (w.t0 + i) * 128, j = j0 + tid, u = j - w.ctx;
         const bool in = j < len;
         const int kst = it % C::kKStages;
@@ -736,67 +736,73 @@ __global__ void __launch_bounds__(320, 1)
         }
       }
       tc_fence_before();
-      named_bar_sync(bar_both, 256);
+      named_bar_sync(bar_all, C::kSoft);
       tc_fence_after();
-      const bool has0 = n > 1 || ((it - 1) & 1) == 0, has1 = n > 1 || ((it - 1) & 1) == 1;
+      // whether warpgroup v had a tile of this segment
+      auto has = [&](int v) { return n >= C::kWG || (v - (it - n) % C::kWG + C::kWG) % C::kWG < n; };
       const bool whole = w.t0 == 0 && w.t1 == w.nt;  // all of the sequence's tiles
       // a partial segment's sums go to the block's first or second place
       float* part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * NR * (D + 2);
-#pragma unroll 1
-      for (int r = threadIdx.x; r < rows; r += 256) {
-        const float m0 = has0 ? -nref_all[r] : -INFINITY, m1 = has1 ? -nref_all[NR + r] : -INFINITY;
-        const float M = fmaxf(m0, m1);
-        float f0 = 0.f, f1 = 0.f, L = 0.f;
-        if (has0) {
-          f0 = fast_exp2(m0 - M);
-          L += ((lsum[r] + lsum[NR + r]) + (lsum[2 * NR + r] + lsum[3 * NR + r])) * f0;
+      for (int r = threadIdx.x; r < rows; r += C::kSoft) {
+        float f[C::kWG], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int v = 0; v < C::kWG; ++v) {
+          f[v] = has(v) ? -nref_all[v * NR + r] : -INFINITY;
+          M = fmaxf(M, f[v]);
         }
-        if (has1) {
-          f1 = fast_exp2(m1 - M);
-          L += ((lsum[4 * NR + r] + lsum[5 * NR + r]) + (lsum[6 * NR + r] + lsum[7 * NR + r])) * f1;
+#pragma unroll
+        for (int v = 0; v < C::kWG; ++v) {
+          f[v] = has(v) ? fast_exp2(f[v] - M) : 0.f;
+          const float* x = lsum + v * 4 * NR + r;
+          if (has(v)) L += ((x[0] + x[NR]) + (x[2 * NR] + x[3 * NR])) * f[v];
         }
         if (whole) {
           const float by = L == 0.f ? 0.f : 1.f / L;  // a row that saw nothing: 0, -infinity
-          f0 *= by;
-          f1 *= by;
+#pragma unroll
+          for (int v = 0; v < C::kWG; ++v) f[v] *= by;
           if (p.lse) p.lse[qb + row_at[r]] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
           part[r * (D + 2) + D] = M;
           part[r * (D + 2) + D + 1] = L;
         }
-        weight[r] = f0;
-        weight[NR + r] = f1;
+#pragma unroll
+        for (int v = 0; v < C::kWG; ++v) weight[v * NR + r] = f[v];
       }
-      named_bar_sync(bar_both, 256);
-      // lane = element of the value; the warpgroups take half of the rows each
+      named_bar_sync(bar_all, C::kSoft);
+      // lane = element of the value; the warpgroups take turns at eight rows
 #pragma unroll 1
-      for (int c0 = wg * (NR / 2); c0 < min(rows, (wg + 1) * (NR / 2)); c0 += 8) {
-        uint32_t a[8], b[8];
-        tmem_ld(lanes + 2 * NR + c0, a);
-        tmem_ld(lanes + 3 * NR + c0, b);
-        tmem_landed(a);
-        tmem_landed(b);
+      for (int c0 = wg * 8; c0 < rows; c0 += C::kWG * 8) {
+        float x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = 0.f;
+#pragma unroll
+        for (int v = 0; v < C::kWG; ++v) {
+          if (!has(v)) continue;  // its O^T is not of this segment
+          uint32_t o[8];
+          tmem_ld(lanes + (C::kWG + v) * NR + c0, o);
+          tmem_landed(o);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = fmaf(__uint_as_float(o[c]), weight[v * NR + c0 + c], x[c]);
+        }
         if (tid < D) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const int r = c0 + c;
             if (r >= rows) break;
-            const float x = (has0 ? __uint_as_float(a[c]) * weight[r] : 0.f) +
-                            (has1 ? __uint_as_float(b[c]) * weight[NR + r] : 0.f);
-            if (whole) p.o[(qb + row_at[r]) * D + tid] = __float2bfloat16(x);
-            else part[r * (D + 2) + tid] = x;
+            if (whole) p.o[(qb + row_at[r]) * D + tid] = __float2bfloat16(x[c]);
+            else part[r * (D + 2) + tid] = x[c];
           }
         }
       }
       tc_fence_before();
-      named_bar_sync(bar_both, 256);  // Q, P and the references are the next segment's
+      named_bar_sync(bar_all, C::kSoft);  // Q, P and the references are the next segment's
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kIssuer) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmem < 32 ? 32 : C::kTmem);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -812,10 +818,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ctx;
   const int nd = new_tokens(p, b, ctx), nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-  long long before, total;
+  int before, total;
   warp_prefix(p, b, before, total);
-  const long long per = run_length(p, total), s0 = before + (long long)h * nt, s1 = s0 + nt;
-  const int first = (int)(s0 / per), n = (int)((s1 - 1) / per) - first + 1;
+  const unsigned per = run_length(p, total), s0 = before + h * nt;
+  const int first = s0 / per, n = nt > 0 ? (int)((s0 + nt - 1) / per) - first + 1 : 0;
   wait_prerequisite();  // every block: the launches that follow rely on this one being over last
   if (rg * nr + r >= nd * p.group || n <= 1) return;
   auto part_of = [&](int i) {
@@ -866,11 +872,10 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, c
   const long long rows = (long long)p.T * p.group;
   p.groups = (int)((rows + NR - 1) / NR);
   p.rows = NR;
-  p.min_run = 2;
   const long long most = (((long long)p.c.max_pages << p.c.log_page) + 127) / 128 * p.B * p.c.Hkv;
-  p.lanes = (int)std::max<long long>(1, std::min<long long>(kMaxBlocks / p.groups, (most + p.min_run - 1) / p.min_run));
+  p.lanes = (int)std::min<long long>(kMaxBlocks / p.groups, most);
   const long long bh = (long long)p.B * p.c.Hkv;
-  if (p.groups > kMaxBlocks || bh > 65535) return cudaErrorInvalidConfiguration;
+  if (p.groups > kMaxBlocks || bh > 65535 || most >= (1ll << 30)) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   tree_attn_kernel<D, F8, NR><<<p.lanes * p.groups, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
