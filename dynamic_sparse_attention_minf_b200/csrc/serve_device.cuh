@@ -31,6 +31,11 @@ __device__ __forceinline__ bool elect_lane() {
   return p != 0;
 }
 
+// Asynchronous copy of four bytes (4-byte aligned), global to shared.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // D(tmem) (+)= A(smem) * B(smem), kind::f8f6f4 (8-bit inputs, fp32 accumulate).
 __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {

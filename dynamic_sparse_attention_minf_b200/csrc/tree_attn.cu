@@ -107,7 +107,7 @@ template <int D, bool F8, int NR>
 struct Cfg {
   // softmax warpgroups, on alternate tiles: four where TMEM and registers allow
   // (one tile's chain of waits is longer than its loads), two otherwise
-  static constexpr int kWG = NR <= 32 ? 4 : 2;
+  static constexpr int kWG = NR == 16 || (NR == 32 && !F8) ? 4 : 2;
   static constexpr int kSoft = 128 * kWG;
   static constexpr int kThreads = kSoft + 96;         // and the issuer, the K and the V producer
   static constexpr int kRowB = D * (F8 ? 1 : 2);       // bytes of a cached row
@@ -141,9 +141,16 @@ struct Cfg {
   static constexpr int kSmem = kOffMisc + 48;
   static constexpr uint32_t kSwizzle = kPitch == 128 ? 2u : 4u;
   static constexpr uint32_t kGroup8 = 8 * kPitch;             // eight rows of a region
-  static constexpr int kTmem = 2 * kWG * NR;                  // S and O of the warpgroups
-  static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, NR, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
-  static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, NR, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
+  // The 8-bit parts of a query (of a weight) lie side by side as more columns of
+  // one product while TMEM has room for them, and are added when read; they
+  // accumulate in turn otherwise.  A product of few columns costs its issue
+  // (about 100 cycles), not its columns.
+  static constexpr int kQStack = F8 && NR <= 32 ? 2 : 1, kPStack = F8 && NR <= 64 ? 3 : 1;
+  static constexpr int kSCols = kQStack * NR, kOCols = kPStack * NR;  // of a warpgroup
+  static constexpr int kOffO = kWG * kSCols;                          // first column of O
+  static constexpr int kTmem = kWG * (kSCols + kOCols) <= 128 ? 128 : kWG * (kSCols + kOCols) <= 256 ? 256 : 512;
+  static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, kSCols, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
+  static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, kOCols, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
   static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
@@ -151,7 +158,7 @@ struct Cfg {
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(24 * NR <= kPB && 20 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
-  static_assert(NR * D * 2 <= kWG * kPB && kTmem >= 32, "the queries as they are in the idle P buffers");
+  static_assert(NR * D * 2 <= kWG * kPB && kWG * (kSCols + kOCols) <= kTmem, "the queries as they are in the idle P buffers");
 };
 
 // Sums each of N values (16 or 32) over the warp's lanes; lane i ends with the
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     // (lane i < pages loads page i): a box costs its warp about 100 cycles to
     // issue, and with pages of 16 rows a tile has 8 or 16 boxes of each.  With K
     // go, in 8 bits, the exponents of the tile's keys and values, four keys per
-    // lane.  Page ids are read two tiles ahead, exponents one.
+    // lane.  No load is waited for: page ids come 32 at a time, a batch ahead.
     const bool is_k = warp == kLoadK;
     const int stages = is_k ? C::kKStages : C::kVStages;
     uint64_t* full = is_k ? k_full : v_full;
@@ -296,35 +303,21 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     while (live && w.next(p)) {
       if (rg * NR >= w.nd * p.group) continue;
       const int len = w.ctx + w.nd;
+      const int log = p.c.log_page, per_tile = 128 >> log, per_batch = 32 / per_tile;
+      const int first = w.t0 * per_tile, end = min(w.t1 * per_tile, (len + (1 << log) - 1) >> log);  // pages
       const int32_t* table = p.c.pages + (long long)w.b * p.c.max_pages;
-      const int per_tile = 128 >> p.c.log_page;
-      // first pool row of this lane's page of tile t; a bad page is reported and page 0 read instead
-      auto fetch = [&](int t, int& pages) {
-        pages = min(per_tile, (len - t * 128 + (1 << p.c.log_page) - 1) >> p.c.log_page);
-        int id = lane < pages ? __ldg(table + t * per_tile + lane) : 0;
-        if (id < 0 || id >= p.c.n_pages) {
-          report(p.status, MINF_ERR_DEVICE_BOUNDS, 111);
-          id = 0;
-        }
-        return (id * p.c.Hkv + w.h) << p.c.log_page;
-      };
-      auto exponents = [&](int row, int pages, uint32_t& ke, uint32_t& ve) {
-        const int pg = (4 * lane) >> p.c.log_page;
-        const int at = __shfl_sync(0xFFFFFFFFu, row, pg) + ((4 * lane) & ((1 << p.c.log_page) - 1));
-        ke = ve = 0;
-        if (pg < pages) {
-          ke = __ldg(reinterpret_cast<const uint32_t*>(p.c.ke + at));
-          ve = __ldg(reinterpret_cast<const uint32_t*>(p.c.ve + at));
-        }
-      };
-      int pages = 0, row = fetch(w.t0, pages), pages_n = 0, row_n = 0;
-      uint32_t ke = 0, ve = 0, ke_n = 0, ve_n = 0;
-      if (w.t0 + 1 < w.t1) row_n = fetch(w.t0 + 1, pages_n);
-      if (F8 && is_k) exponents(row, pages, ke, ve);
+      auto fetch = [&](int pg) { return pg + lane < end ? __ldg(table + pg + lane) : 0; };
+      int row = 0, ids = fetch(first);  // first pool row of this lane's page of the batch; the next batch
       for (int t = w.t0; t < w.t1; ++t, ++n) {
-        int pages_2 = 0, row_2 = 0;
-        if (t + 2 < w.t1) row_2 = fetch(t + 2, pages_2);
-        if (F8 && is_k) exponents(row_n, pages_n, ke_n, ve_n);
+        const int at = (t - w.t0) % per_batch * per_tile, pages = min(per_tile, end - t * per_tile);
+        if (at == 0) {
+          if (ids < 0 || ids >= p.c.n_pages) {  // reported, and page 0 read instead
+            report(p.status, MINF_ERR_DEVICE_BOUNDS, 111);
+            ids = 0;
+          }
+          row = (ids * p.c.Hkv + w.h) << log;
+          ids = fetch(t * per_tile + 32);
+        }
         const int st = n % stages;
         if (n >= stages)
           mbar_wait_or_abort(&empty[st], ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
@@ -333,25 +326,24 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
           break;
         }
         if (F8 && is_k) {
-          uint32_t* e = reinterpret_cast<uint32_t*>(smem + C::kOffExp + st * C::kExpB) + lane;
-          e[0] = ke;
-          e[32] = ve;
+          const int pg = (4 * lane) >> log;
+          const int from = __shfl_sync(0xFFFFFFFFu, row, at + pg) + ((4 * lane) & ((1 << log) - 1));
+          if (pg < pages) {
+            const uint32_t e = smem_u32(smem + C::kOffExp + st * C::kExpB + lane * 4);
+            cp_async4(e, p.c.ke + from);
+            cp_async4(e + 128, p.c.ve + from);
+          }
+          cp_async_mbar_arrive(&full[st]);
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (pages << p.c.log_page) * C::kRowB);
-        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (pages << log) * C::kRowB);
+        const int from = __shfl_sync(0xFFFFFFFFu, row, (at + lane) & 31);
         if (lane < pages) {
-          uint8_t* dst = ring + st * C::kTileB + (lane << p.c.log_page) * C::kPitch;
+          uint8_t* dst = ring + st * C::kTileB + (lane << log) * C::kPitch;
 #pragma unroll
-          for (int r = 0; r < C::kRegions; ++r) tma_load_2d(dst + r * C::kRegion, map, &full[st], r * 64, row);
+          for (int r = 0; r < C::kRegions; ++r) tma_load_2d(dst + r * C::kRegion, map, &full[st], r * 64, from);
         }
         __syncwarp();
-        pages = pages_n;
-        row = row_n;
-        pages_n = pages_2;
-        row_n = row_2;
-        ke = ke_n;
-        ve = ve_n;
       }
     }
     if (lane == 0) {  // never exit with copies in flight
@@ -372,10 +364,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
       if (__any_sync(0xFFFFFFFFu, *abort)) return;
       tc_fence_after();
       const uint32_t v = smem_u32(smem + C::kOffV + st * C::kTileB), pb = smem_u32(smem + C::kOffP + wg * C::kPB);
-      const uint32_t d = tmem + (C::kWG + wg) * NR;
+      const uint32_t d = tmem + C::kOffO + wg * C::kOCols;
       if (elect_lane()) {
 #pragma unroll
-        for (int part = 0; part < C::kPParts; ++part)
+        for (int part = 0; part < C::kPParts / C::kPStack; ++part)
 #pragma unroll
           for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
             constexpr int kKeys = F8 ? 32 : 16;
@@ -403,15 +395,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         const uint32_t k = smem_u32(smem + C::kOffK + st * C::kTileB);
         if (elect_lane()) {
 #pragma unroll
-          for (int part = 0; part < C::kQParts; ++part)
+          for (int part = 0; part < C::kQParts / C::kQStack; ++part)
 #pragma unroll
             for (int kk = 0; kk < C::kRowB / 32; ++kk) {
               const uint64_t a = sdesc(k + (kk * 32 / C::kPitch) * C::kRegion + (kk * 32) % C::kPitch, 16, C::kGroup8,
                                        C::kSwizzle);
-              const uint64_t b = sdesc(q0 + part * C::kQPart + kk * 2 * NR * 16, NR * 16, 128, 0);
+              const uint64_t b = sdesc(q0 + part * C::kQPart + kk * 2 * C::kSCols * 16, C::kSCols * 16, 128, 0);
               const uint32_t acc = part > 0 || kk > 0;
-              if constexpr (F8) umma_ss_f8(tmem + wg * NR, a, b, C::kIdescS, acc);
-              else umma_ss(tmem + wg * NR, a, b, C::kIdescS, acc);
+              if constexpr (F8) umma_ss_f8(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
+              else umma_ss(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
             }
           umma_commit(&s_full[wg]);
           umma_commit(&k_empty[st]);
@@ -438,7 +430,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     // every later wait ends at once, and the barriers below keep their counts.
     const int wg = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_col = lanes + wg * NR, o_col = lanes + (C::kWG + wg) * NR;
+    const uint32_t s_col = lanes + wg * C::kSCols, o_col = lanes + C::kOffO + wg * C::kOCols;
     // the references, negated: [kWG][NR]
     float* nref_all = reinterpret_cast<float*>(smem + C::kOffRef);
     float* nref = nref_all + wg * NR;
@@ -522,9 +514,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
             const uint32_t lo =
                 __nv_cvt_float2_to_fp8x2(make_float2(a.x - back.x, a.y - back.y), __NV_SATFINITE, __NV_E4M3);
             const int byte = lane * E + e;
-            uint8_t* q = smem + C::kOffQ + (byte / 16) * NR * 16 + r * 16 + byte % 16;
+            uint8_t* q = smem + C::kOffQ + (byte / 16) * C::kSCols * 16 + r * 16 + byte % 16;
             *reinterpret_cast<uint16_t*>(q) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(q + C::kQPart) = (uint16_t)lo;
+            *reinterpret_cast<uint16_t*>(q + (C::kQStack > 1 ? NR * 16 : C::kQPart)) = (uint16_t)lo;
           }
           if (lane == 0) fac[r] = bad ? NAN : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
         }
@@ -558,6 +550,21 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         }
         mbar_wait_or_abort(&s_full[wg], uses & 1, abort, p.status, 123);
         tc_fence_after();
+        // scores of rows c0 .. of the thread's key
+        auto scores = [&](int c0, auto& s) {
+          tmem_ld(s_col + c0, s);
+          if constexpr (C::kQStack > 1) {
+            typename std::remove_reference<decltype(s)>::type lo;
+            tmem_ld(s_col + NR + c0, lo);
+            tmem_landed(s);
+            tmem_landed(lo);
+#pragma unroll
+            for (int c = 0; c < (int)(sizeof(s) / 4); ++c)
+              s[c] = __float_as_uint(__uint_as_float(s[c]) + __uint_as_float(lo[c]));
+          } else {
+            tmem_landed(s);
+          }
+        };
         // From the tile's scores s to the exponents of their weights, two rows at a
         // time: s scale log2(e) + lv - reference, -infinity where the row does not
         // see the key.
@@ -594,8 +601,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll 1
               for (int c0 = 0; c0 < NR; c0 += 8) {
                 uint32_t s[8];
-                tmem_ld(s_col + c0, s);
-                tmem_landed(s);
+                scores(c0, s);
                 float mine = 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; c += 2) {
@@ -624,12 +630,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
               named_bar_sync(bar_wg, 128);
               if (!first) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < NR; c0 += 8) {
+                for (int c0 = 0; c0 < C::kOCols; c0 += 8) {
                   uint32_t o[8];
                   tmem_ld(o_col + c0, o);
                   tmem_landed(o);
 #pragma unroll
-                  for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * shrink[c0 + c]);
+                  for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * shrink[c0 % NR + c]);
                   tmem_st(o_col + c0, o);
                 }
                 tmem_wait_st();
@@ -638,8 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll
                 for (int c0 = 0; c0 < NR; c0 += 16) {
                   uint32_t s[16];
-                  tmem_ld(s_col + c0, s);
-                  tmem_landed(s);
+                  scores(c0, s);
 #pragma unroll
                   for (int c = 0; c < 16; c += 2) {
                     const int r = c0 + c;
@@ -660,8 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll
             for (int c0 = 0; c0 < NR; c0 += C::kCh) {
               uint32_t s[C::kCh];
-              tmem_ld(s_col + c0, s);
-              tmem_landed(s);
+              scores(c0, s);
               constexpr int kStep = F8 ? 16 : 8;
 #pragma unroll
               for (int g = 0; g < C::kCh; g += kStep) {
@@ -778,11 +782,14 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll
         for (int v = 0; v < C::kWG; ++v) {
           if (!has(v)) continue;  // its O^T is not of this segment
-          uint32_t o[8];
-          tmem_ld(lanes + (C::kWG + v) * NR + c0, o);
-          tmem_landed(o);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = fmaf(__uint_as_float(o[c]), weight[v * NR + c0 + c], x[c]);
+          for (int q = 0; q < C::kPStack; ++q) {
+            uint32_t o[8];
+            tmem_ld(lanes + C::kOffO + v * C::kOCols + q * NR + c0, o);
+            tmem_landed(o);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] = fmaf(__uint_as_float(o[c]), weight[v * NR + c0 + c], x[c]);
+          }
         }
         if (tid < D) {
 #pragma unroll
