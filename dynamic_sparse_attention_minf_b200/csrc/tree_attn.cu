@@ -60,11 +60,10 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
   return nd > 0 ? (ctx + nd + 127) >> 7 : 0;
 }
 
-// Tiles before sequence b, and in all, of the warp's choice of b.
+// Tiles before sequence `upto`, and in all, for a whole warp.
 __device__ __forceinline__ void warp_prefix(const TreeParams& p, int upto, int& before, int& total) {
-  const int lane = threadIdx.x & 31;
   int a = 0, t = 0;
-  for (int b = lane; b < p.B; b += 32) {
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
     const int n = tiles_of(p, b);
     t += n;
     if (b < upto) a += n;
@@ -82,21 +81,20 @@ __device__ __forceinline__ int run_length(const TreeParams& p, int total) {
 // walks it by itself.
 struct Walk {
   int g, g1, base;  // base: first tile of sequence b
-  int b, nt;        // nt: tiles per head of sequence b
-  // the current segment: tiles [t0, t1) of KV head h of sequence b
-  int h, t0, t1, ctx, nd;
+  int b, nt, ctx, nd;  // sequence b: tiles per head, context and new tokens
+  int h, t0, t1;       // the current segment: tiles [t0, t1) of KV head h
   __device__ __forceinline__ bool next(const TreeParams& p) {
     if (g >= g1) return false;
     while (g >= base + nt * p.c.Hkv) {
       base += nt * p.c.Hkv;
       ++b;
-      nt = tiles_of(p, b);
+      nd = new_tokens(p, b, ctx);
+      nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
     }
     const unsigned x = g - base;
     h = x / (unsigned)nt;
     t0 = x - h * nt;
     t1 = min(nt, t0 + (g1 - g));
-    nd = new_tokens(p, b, ctx);
     g += t1 - t0;
     return true;
   }
@@ -238,42 +236,48 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     }
   } else if (warp == 0) {
     // this block's run of the tile list, and the sequence that it begins in
-    int before, total;
-    warp_prefix(p, 0, before, total);
+    // (lane i looks at sequences i, i + 32, ...; a batch of up to 32 is read once)
+    int ctx = 0, nd = lane < p.B ? new_tokens(p, lane, ctx) : 0;
+    bool bad = nd < 0;
+    int n = nd > 0 ? (ctx + nd + 127) >> 7 : 0, total = n;
+    for (int b = lane + 32; b < p.B; b += 32) {
+      int c;
+      const int d = new_tokens(p, b, c);
+      bad = bad || d < 0;
+      total += d > 0 ? (c + d + 127) >> 7 : 0;
+    }
+    if (bad && blockIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
+    total = __reduce_add_sync(0xFFFFFFFFu, total) * p.c.Hkv;
     const int per = run_length(p, total);
     Walk w;
     w.g = min(total, part_lane * per);
     w.g1 = min(total, w.g + per);
     w.base = 0;
-    w.b = 0;
-    w.nt = 0;
-    if (w.g < w.g1) {
-      for (int b0 = 0;; b0 += 32) {
-        const int n = b0 + lane < p.B ? tiles_of(p, b0 + lane) : 0;
-        int incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > w.g);
-        if (past) {
-          const int at = __ffs(past) - 1;
-          w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - __shfl_sync(0xFFFFFFFFu, n, at)) * p.c.Hkv;
-          w.b = b0 + at;
-          w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
-          break;
-        }
-        w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
+    w.b = w.nt = w.ctx = w.nd = 0;
+    for (int b0 = 0; w.g < w.g1; b0 += 32) {
+      if (b0 > 0) {
+        nd = b0 + lane < p.B ? new_tokens(p, b0 + lane, ctx) : 0;
+        n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
       }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > w.g);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        w.b = b0 + at;
+        w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
+        w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - w.nt) * p.c.Hkv;
+        w.ctx = __shfl_sync(0xFFFFFFFFu, ctx, at);
+        w.nd = __shfl_sync(0xFFFFFFFFu, nd, at);
+        break;
+      }
+      w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
     }
     if (lane == 0) *start = w;
-    if (blockIdx.x == 0) {
-      for (int b = lane; b < p.B; b += 32) {
-        int ctx;
-        if (new_tokens(p, b, ctx) < 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -835,6 +839,12 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
     const long long slot = 2ll * ((first + i) * p.groups + rg) + (i == 0 ? 1 : 0);
     return p.part + (slot * p.rows + r) * (D + 2);
   };
+  // the first parts' sums are on their way while the weights are formed
+  constexpr int kAhead = 8;
+  const int g = threadIdx.x / D, e = threadIdx.x % D;
+  float x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = g + i * G < n ? part_of(g + i * G)[e] : 0.f;
   float m = -INFINITY, l = 0.f;
   if (threadIdx.x < n) {
     m = part_of(threadIdx.x)[D];
@@ -853,10 +863,12 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
   __syncthreads();
   if (lane == 0) red[warp] = L;
-  const int g = threadIdx.x / D, e = threadIdx.x % D;
   float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (g + i * G < n) a = fmaf(x[i], wt[g + i * G], a);
 #pragma unroll 8
-  for (int i = g; i < n; i += G) a = fmaf(part_of(i)[e], wt[i], a);
+  for (int i = g + kAhead * G; i < n; i += G) a = fmaf(part_of(i)[e], wt[i], a);
   acc[g][e] = a;
   __syncthreads();
   if (g > 0) return;
