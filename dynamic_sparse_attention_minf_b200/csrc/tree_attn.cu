@@ -107,7 +107,11 @@ struct Cfg {
   // (one tile's chain of waits is longer than its loads), two otherwise
   static constexpr int kWG = NR == 16 || (NR == 32 && !F8) ? 4 : 2;
   static constexpr int kSoft = 128 * kWG;
-  static constexpr int kThreads = kSoft + 96;         // and the issuer, the K and the V producer
+  // With 128 rows a softmax thread's sums alone take 128 registers: the fourth
+  // warp of the issuer and the producers idles, so that a whole warpgroup hands
+  // registers on (168 at launch; 208 and 88: 256 * 208 + 128 * 88 = 384 * 168).
+  static constexpr bool kSplitRegs = NR == 128;
+  static constexpr int kThreads = kSoft + (kSplitRegs ? 128 : 96);  // and the issuer, the K and the V producer
   static constexpr int kRowB = D * (F8 ? 1 : 2);       // bytes of a cached row
   static constexpr int kPitch = kRowB < 128 ? kRowB : 128;  // row pitch within a swizzled region
   static constexpr int kRegions = kRowB / kPitch;
@@ -181,6 +185,11 @@ __device__ __forceinline__ float lane_totals(float (&v)[N]) {
     }
   }
   return v[0];
+}
+
+template <bool kOn>
+__device__ __forceinline__ void fewer_registers() {
+  if constexpr (kOn) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
 }
 
 template <int D, bool F8, int NR>
@@ -287,13 +296,16 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
   Walk w = *start;
   __syncthreads();  // the run's place is the P buffer
 
-  if (warp == kLoadK || warp == kLoadV) {
+  if (warp > kLoadV) {
+    fewer_registers<C::kSplitRegs>();
+  } else if (warp == kLoadK || warp == kLoadV) {
     // ----------------------------------------------------------- producers
     // One warp loads the K tiles and one the V tiles, each tile page by page
     // (lane i < pages loads page i): a box costs its warp about 100 cycles to
     // issue, and with pages of 16 rows a tile has 8 or 16 boxes of each.  With K
     // go, in 8 bits, the exponents of the tile's keys and values, four keys per
     // lane.  No load is waited for: page ids come 32 at a time, a batch ahead.
+    fewer_registers<C::kSplitRegs>();
     const bool is_k = warp == kLoadK;
     const int stages = is_k ? C::kKStages : C::kVStages;
     uint64_t* full = is_k ? k_full : v_full;
@@ -358,6 +370,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     __syncwarp();
   } else if (warp == kIssuer) {
     // --------------------------------------------------------- MMA issuer
+    fewer_registers<C::kSplitRegs>();
     const uint32_t q0 = smem_u32(smem + C::kOffQ);
     int it = 0, segs = 0;
     // O^T of the tile's warpgroup (+)= V^T P
@@ -432,6 +445,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     // ------------------------------------------------------------- softmax
     // A failed wait is not followed up here: the status word and *abort are set,
     // every later wait ends at once, and the barriers below keep their counts.
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int wg = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lanes + wg * C::kSCols, o_col = lanes + C::kOffO + wg * C::kOCols;
