@@ -24,6 +24,19 @@ __device__ __forceinline__ void mbar_wait_or_abort(uint64_t* bar, uint32_t parit
   }
 }
 
+// Whether the phase with the given parity is over; never suspends the thread.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t p;

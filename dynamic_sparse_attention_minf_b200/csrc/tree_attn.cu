@@ -159,7 +159,7 @@ struct Cfg {
   static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(24 * NR <= kPB && 20 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
+  static_assert(24 * NR <= kPB && 4 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
   static_assert(NR * D * 2 <= kWG * kPB && kWG * (kSCols + kOCols) <= kTmem, "the queries as they are in the idle P buffers");
 };
 
@@ -371,68 +371,89 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
   } else if (warp == kIssuer) {
     // --------------------------------------------------------- MMA issuer
     fewer_registers<C::kSplitRegs>();
-    const uint32_t q0 = smem_u32(smem + C::kOffQ);
-    int it = 0, segs = 0;
-    // O^T of the tile's warpgroup (+)= V^T P
-    auto issue_pv = [&](int i, bool first) {
-      const int wg = i % C::kWG, st = i % C::kVStages;
-      mbar_wait_or_abort(&p_full[wg], (i / C::kWG) & 1, abort, p.status, 117);
-      mbar_wait_or_abort(&v_full[st], (i / C::kVStages) & 1, abort, p.status, 118);
-      if (__any_sync(0xFFFFFFFFu, *abort)) return;
-      tc_fence_after();
-      const uint32_t v = smem_u32(smem + C::kOffV + st * C::kTileB), pb = smem_u32(smem + C::kOffP + wg * C::kPB);
-      const uint32_t d = tmem + C::kOffO + wg * C::kOCols;
-      if (elect_lane()) {
-#pragma unroll
-        for (int part = 0; part < C::kPParts / C::kPStack; ++part)
-#pragma unroll
-          for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
-            constexpr int kKeys = F8 ? 32 : 16;
-            const uint64_t a = sdesc(v + kk * kKeys * C::kPitch, C::kRegion, C::kGroup8, C::kSwizzle);
-            const uint64_t b = sdesc(pb + part * C::kPPart + kk * kKeys * 16, 128, 2048, 0);
-            const uint32_t acc = part > 0 || kk > 0 || !first;
-            if constexpr (F8) umma_ss_f8(d, a, b, C::kIdescO, acc);
-            else umma_ss(d, a, b, C::kIdescO, acc);
-          }
-        umma_commit(&v_empty[st]);
-        umma_commit(&pv_done[wg]);
-      }
-      __syncwarp();
-    };
+    // operand descriptors: a base per buffer, plus constants (the start-address
+    // field holds address / 16 and never carries out)
+    const uint64_t q0 = sdesc(smem_u32(smem + C::kOffQ), C::kSCols * 16, 128, 0);
+    const uint64_t p0 = sdesc(smem_u32(smem + C::kOffP), 128, 2048, 0);
+    const uint64_t k0 = sdesc(smem_u32(smem + C::kOffK), 16, C::kGroup8, C::kSwizzle);
+    const uint64_t v0 = sdesc(smem_u32(smem + C::kOffV), C::kRegion, C::kGroup8, C::kSwizzle);
+    auto ready = [&](uint64_t* bar, int parity) { return (bool)__all_sync(0xFFFFFFFFu, mbar_poll(bar, parity)); };
+    int it0 = 0, segs = 0;
     while (!__any_sync(0xFFFFFFFFu, *abort) && w.next(p)) {
       if (rg * NR >= w.nd * p.group) continue;
       mbar_wait_or_abort(q_full, segs & 1, abort, p.status, 119);
       ++segs;
+      // Of the segment's n tiles, s have their scores issued, pd their weights
+      // formed and pv their values' product issued.  Whatever is ready goes next,
+      // scores first, so that no warpgroup waits behind another's product.
       const int n = w.t1 - w.t0;
-      for (int i = 0; i < n; ++i, ++it) {
-        const int wg = it % C::kWG, st = it % C::kKStages;
-        mbar_wait_or_abort(&k_full[st], (it / C::kKStages) & 1, abort, p.status, 120);
-        if (__any_sync(0xFFFFFFFFu, *abort)) break;
-        tc_fence_after();
-        const uint32_t k = smem_u32(smem + C::kOffK + st * C::kTileB);
-        if (elect_lane()) {
-#pragma unroll
-          for (int part = 0; part < C::kQParts / C::kQStack; ++part)
-#pragma unroll
-            for (int kk = 0; kk < C::kRowB / 32; ++kk) {
-              const uint64_t a = sdesc(k + (kk * 32 / C::kPitch) * C::kRegion + (kk * 32) % C::kPitch, 16, C::kGroup8,
-                                       C::kSwizzle);
-              const uint64_t b = sdesc(q0 + part * C::kQPart + kk * 2 * C::kSCols * 16, C::kSCols * 16, 128, 0);
-              const uint32_t acc = part > 0 || kk > 0;
-              if constexpr (F8) umma_ss_f8(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
-              else umma_ss(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
-            }
-          umma_commit(&s_full[wg]);
-          umma_commit(&k_empty[st]);
+      int s = 0, pd = 0, pv = 0, idle = 0;
+      unsigned long long since = 0;
+      while (pv < n) {
+        bool moved = false;
+        if (pd < s && ready(&p_full[(it0 + pd) % C::kWG], (it0 + pd) / C::kWG & 1)) {
+          ++pd;
+          tc_fence_after();
+          moved = true;
         }
-        __syncwarp();
-        // scores run ahead of the weights by one tile less than there are
-        // warpgroups: PV(it - kWG), before this, has waited for the tile whose S
-        // buffer this one takes
-        if (i >= C::kWG - 1) issue_pv(it - (C::kWG - 1), i - (C::kWG - 1) < C::kWG);
+        const int is = it0 + s, ks = is % C::kKStages, iv = it0 + pv, vs = iv % C::kVStages;
+        if (s < n && s - pd < C::kWG && ready(&k_full[ks], is / C::kKStages & 1)) {
+          // the scores' buffer is that of tile s - kWG, whose weights are formed
+          const int wg = is % C::kWG;
+          const uint64_t k = k0 + (uint32_t)(ks * (C::kTileB / 16));
+          if (elect_lane()) {
+#pragma unroll
+            for (int part = 0; part < C::kQParts / C::kQStack; ++part)
+#pragma unroll
+              for (int kk = 0; kk < C::kRowB / 32; ++kk) {
+                const uint64_t a = k + (uint32_t)(((kk * 32 / C::kPitch) * C::kRegion + (kk * 32) % C::kPitch) / 16);
+                const uint64_t b = q0 + (uint32_t)((part * C::kQPart + kk * 2 * C::kSCols * 16) / 16);
+                const uint32_t acc = part > 0 || kk > 0;
+                if constexpr (F8) umma_ss_f8(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
+                else umma_ss(tmem + wg * C::kSCols, a, b, C::kIdescS, acc);
+              }
+            umma_commit(&s_full[wg]);
+            umma_commit(&k_empty[ks]);
+          }
+          __syncwarp();
+          ++s;
+          moved = true;
+        } else if (pv < pd && ready(&v_full[vs], iv / C::kVStages & 1)) {
+          // O^T of the tile's warpgroup (+)= V^T P
+          const int wg = iv % C::kWG;
+          const uint64_t v = v0 + (uint32_t)(vs * (C::kTileB / 16)), pb = p0 + (uint32_t)(wg * (C::kPB / 16));
+          const uint32_t d = tmem + C::kOffO + wg * C::kOCols;
+          if (elect_lane()) {
+#pragma unroll
+            for (int part = 0; part < C::kPParts / C::kPStack; ++part)
+#pragma unroll
+              for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
+                constexpr int kKeys = F8 ? 32 : 16;
+                const uint64_t a = v + (uint32_t)(kk * kKeys * C::kPitch / 16);
+                const uint64_t b = pb + (uint32_t)((part * C::kPPart + kk * kKeys * 16) / 16);
+                const uint32_t acc = part > 0 || kk > 0 || pv >= C::kWG;
+                if constexpr (F8) umma_ss_f8(d, a, b, C::kIdescO, acc);
+                else umma_ss(d, a, b, C::kIdescO, acc);
+              }
+            umma_commit(&v_empty[vs]);
+            umma_commit(&pv_done[wg]);
+          }
+          __syncwarp();
+          ++pv;
+          moved = true;
+        }
+        if (moved) {
+          idle = 0;
+        } else if ((++idle & 63) == 0) {  // bounded, as every wait
+          if (idle == 64) since = globaltimer();
+          if (!*abort && globaltimer() - since > kWaitLimitNs) {
+            *abort = 1;
+            report(p.status, MINF_ERR_DEVICE_TIMEOUT, 117);
+          }
+          if (__any_sync(0xFFFFFFFFu, *abort)) break;
+        }
       }
-      for (int i = max(0, n - (C::kWG - 1)); i < n && !__any_sync(0xFFFFFFFFu, *abort); ++i)
-        issue_pv(it - n + i, i < C::kWG);
+      it0 += n;
     }
     if (elect_lane()) umma_commit(mma_done);
     __syncwarp();
@@ -460,8 +481,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     float* wmax = reinterpret_cast<float*>(pbuf);             // [4][NR] while P is idle
     float* shrink = wmax + 4 * NR;                            // [NR]
     float* nwas = shrink + NR;                                // [NR]
-    float* lsum = reinterpret_cast<float*>(smem + C::kOffQ);  // [kWG][4][NR] while Q is idle
-    float* weight = lsum + C::kWG * 4 * NR;                   // [kWG][NR]
+    float* lsum = reinterpret_cast<float*>(pbuf);             // [4][NR] after the segment's last tile
+    float* weight = reinterpret_cast<float*>(smem + C::kOffQ);  // [kWG][NR] while Q is idle
     const int bar_wg = 1 + wg, bar_all = 1 + C::kWG;
     int it = 0, uses = 0;  // tiles of the block so far, and those of this warpgroup
     while (w.next(p)) {
@@ -689,27 +710,41 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
               for (int g = 0; g < C::kCh; g += kStep) {
                 uint32_t out[C::kPParts][4];
 #pragma unroll
-                for (int c = 0; c < kStep; c += 2) {
-                  const int r = c0 + g + c;
-                  float t0, t1;
-                  exponent2(masked, s[g + c], s[g + c + 1], r, nref, t0, t1);
-                  top = fmaxf(top, fmaxf(t0, t1));
-                  const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                for (int c = 0; c < kStep; c += 4) {
+                  uint32_t h[2];  // four weights as pairs of bf16, or of half
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const int r = c0 + g + c + 2 * x;
+                    float t0, t1;
+                    exponent2(masked, s[g + c + 2 * x], s[g + c + 2 * x + 1], r, nref, t0, t1);
+                    top = fmaxf(top, fmaxf(t0, t1));
+                    const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                    if constexpr (F8) {
+                      l[r / 2] = f32x2_fma(f32x2_pack(p0, p1), f32x2_pack(inv, inv), l[r / 2]);
+                      const __half2 two = __floats2half2_rn(p0, p1);
+                      h[x] = *reinterpret_cast<const uint32_t*>(&two);
+                    } else {
+                      l[r / 2] = f32x2_add(l[r / 2], f32x2_pack(p0, p1));
+                      h[x] = pack_bf16x2(p0, p1);
+                    }
+                  }
                   if constexpr (F8) {
-                    l[r / 2] = f32x2_fma(f32x2_pack(p0, p1), f32x2_pack(inv, inv), l[r / 2]);
-                    __half2 h = __floats2half2_rn(p0, p1);  // e5m2 is the upper byte of a half
+                    // e5m2 is the upper byte of a half: each part is the remainder
+                    // rounded there (half a step up, in magnitude), and leaves an
+                    // exact remainder.  A NaN weight may be lost here, not in l.
 #pragma unroll
                     for (int q = 0; q < 3; ++q) {
-                      const uint32_t e =
-                          __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E5M2);
-                      if (c & 2) out[q][c / 4] |= e << 16;
-                      else out[q][c / 4] = e;
-                      const uint32_t wide = __byte_perm(e, 0, 0x1404);
-                      h = __hsub2(h, *reinterpret_cast<const __half2*>(&wide));
+                      const uint32_t a = h[0] + 0x00800080u, b = h[1] + 0x00800080u;
+                      out[q][c / 4] = __byte_perm(a, b, 0x7531);
+                      const uint32_t ta = a & 0xff00ff00u, tb = b & 0xff00ff00u;
+                      const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&h[0]), *reinterpret_cast<const __half2*>(&ta));
+                      const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&h[1]), *reinterpret_cast<const __half2*>(&tb));
+                      h[0] = *reinterpret_cast<const uint32_t*>(&ra);
+                      h[1] = *reinterpret_cast<const uint32_t*>(&rb);
                     }
                   } else {
-                    l[r / 2] = f32x2_add(l[r / 2], f32x2_pack(p0, p1));
-                    out[0][c / 2] = pack_bf16x2(p0, p1);
+                    out[0][c / 2] = h[0];
+                    out[0][c / 2 + 1] = h[1];
                   }
                 }
 #pragma unroll
@@ -754,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kSum; c += 2) f32x2_unpack(l[(c0 + c) / 2], v[c], v[c + 1]);
           const float t = lane_totals<kSum>(v);
-          if (kSum == 32 || (lane & 1) == 0) lsum[(wg * 4 + (warp & 3)) * NR + c0 + (kSum == 32 ? lane : lane / 2)] = t;
+          if (kSum == 32 || (lane & 1) == 0) lsum[(warp & 3) * NR + c0 + (kSum == 32 ? lane : lane / 2)] = t;
         }
       }
       tc_fence_before();
@@ -775,7 +810,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
 #pragma unroll
         for (int v = 0; v < C::kWG; ++v) {
           f[v] = has(v) ? fast_exp2(f[v] - M) : 0.f;
-          const float* x = lsum + v * 4 * NR + r;
+          const float* x = reinterpret_cast<const float*>(smem + C::kOffP + v * C::kPB) + r;
           if (has(v)) L += ((x[0] + x[NR]) + (x[2 * NR] + x[3 * NR])) * f[v];
         }
         if (whole) {
