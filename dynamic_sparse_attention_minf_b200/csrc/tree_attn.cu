@@ -27,10 +27,12 @@
 //    hold bf16's 8 bits; the weight (times the value's power of two) into three
 //    e5m2 parts, 9 bits, whose range of 2^32 keeps small weights beside a
 //    dominant one.
-//  * The tiles of all sequences and heads form one list, cut into equal runs, one
-//    per block: ragged batches and single long sequences both fill the GPU.  A
-//    run that covers part of a sequence leaves its sums in the workspace, and a
-//    second kernel, launched ahead of time, joins them in order.
+//  * The work is cut evenly over the blocks, one per SM.  Few sequences (at most
+//    one per block, counted with their KV heads) are each cut into pieces, so that
+//    no block pays for two sequences' beginning and end.  Many form one list of
+//    tiles, cut into equal runs, so that a ragged batch loads every block alike.
+//    What covers part of a sequence leaves its sums in the workspace, and a second
+//    kernel, launched ahead of time, joins them in order.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -60,31 +62,52 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
   return nd > 0 ? (ctx + nd + 127) >> 7 : 0;
 }
 
-// Tiles before sequence `upto`, and in all, for a whole warp.
-__device__ __forceinline__ void warp_prefix(const TreeParams& p, int upto, int& before, int& total) {
-  int a = 0, t = 0;
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+__device__ __forceinline__ int ceil_div(int a, int b) { return (unsigned)(a + b - 1) / (unsigned)b; }
+
+// How the work is cut, for a whole warp: in runs of `per` tiles of the list
+// (sequence-major, then KV head, then tile), or, with at most one sequence and
+// head per block, each of these into pieces of at most `per` tiles.  `units` of
+// a sequence's head are its tiles or its pieces.
+struct Cut {
+  int per;
+  bool pieces;
+  __device__ __forceinline__ int units(int nt) const { return pieces ? ceil_div(nt, per) : nt; }
+};
+// n0: tiles of sequence `lane` (read by the caller)
+__device__ __forceinline__ Cut make_cut(const TreeParams& p, int n0) {
+  const int lane = threadIdx.x & 31;
+  int total = n0, live = n0 > 0;
+  for (int b = lane + 32; b < p.B; b += 32) {
     const int n = tiles_of(p, b);
-    t += n;
-    if (b < upto) a += n;
+    total += n;
+    live += n > 0;
   }
-  before = __reduce_add_sync(0xFFFFFFFFu, a) * p.c.Hkv;
-  total = __reduce_add_sync(0xFFFFFFFFu, t) * p.c.Hkv;
-}
-// tiles of a block's run
-__device__ __forceinline__ int run_length(const TreeParams& p, int total) {
-  return max(1, (int)((unsigned)(total + p.lanes - 1) / (unsigned)p.lanes));
+  total = __reduce_add_sync(0xFFFFFFFFu, total) * p.c.Hkv;
+  live = __reduce_add_sync(0xFFFFFFFFu, live) * p.c.Hkv;
+  Cut c{max(1, ceil_div(total, p.lanes)), live <= p.lanes};
+  while (c.pieces) {  // longer pieces, by a sixteenth at least, until there is a block for each
+    int k = ceil_div(n0, c.per);
+    for (int b = lane + 32; b < p.B; b += 32) k += ceil_div(tiles_of(p, b), c.per);
+    k = __reduce_add_sync(0xFFFFFFFFu, k) * p.c.Hkv;
+    if (k <= p.lanes) break;
+    c.per = max(c.per + c.per / 16 + 1, (int)(((long long)c.per * k + p.lanes - 1) / p.lanes));
+  }
+  return c;
 }
 
-// A block's run [g, g1) of the tile list (sequence-major, then KV head, then
-// tile), walked one (sequence, head) segment at a time; every role of the block
-// walks it by itself.
+// A block's share, walked one (sequence, head) segment at a time; every role of
+// the block walks it by itself.
 struct Walk {
-  int g, g1, base;  // base: first tile of sequence b
+  int g, g1, base;     // the run [g, g1) of the tile list; base: first tile of sequence b
   int b, nt, ctx, nd;  // sequence b: tiles per head, context and new tokens
   int h, t0, t1;       // the current segment: tiles [t0, t1) of KV head h
+  bool pieces;         // one segment only, set up already
   __device__ __forceinline__ bool next(const TreeParams& p) {
     if (g >= g1) return false;
+    if (pieces) {
+      g = g1;
+      return true;
+    }
     while (g >= base + nt * p.c.Hkv) {
       base += nt * p.c.Hkv;
       ++b;
@@ -244,47 +267,58 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
       prefetch_tmap(&tmV);
     }
   } else if (warp == 0) {
-    // this block's run of the tile list, and the sequence that it begins in
-    // (lane i looks at sequences i, i + 32, ...; a batch of up to 32 is read once)
+    // this block's share, and the sequence that it begins in (lane i looks at
+    // sequences i, i + 32, ...; a batch of up to 32 is read once)
     int ctx = 0, nd = lane < p.B ? new_tokens(p, lane, ctx) : 0;
-    bool bad = nd < 0;
-    int n = nd > 0 ? (ctx + nd + 127) >> 7 : 0, total = n;
-    for (int b = lane + 32; b < p.B; b += 32) {
-      int c;
-      const int d = new_tokens(p, b, c);
-      bad = bad || d < 0;
-      total += d > 0 ? (c + d + 127) >> 7 : 0;
-    }
-    if (bad && blockIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
-    total = __reduce_add_sync(0xFFFFFFFFu, total) * p.c.Hkv;
-    const int per = run_length(p, total);
-    Walk w;
-    w.g = min(total, part_lane * per);
-    w.g1 = min(total, w.g + per);
-    w.base = 0;
-    w.b = w.nt = w.ctx = w.nd = 0;
-    for (int b0 = 0; w.g < w.g1; b0 += 32) {
+    int n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+    const Cut cut = make_cut(p, n);
+    const int target = part_lane * (cut.pieces ? 1 : cut.per);  // first unit of the share
+    Walk w{};
+    w.pieces = cut.pieces;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
       if (b0 > 0) {
         nd = b0 + lane < p.B ? new_tokens(p, b0 + lane, ctx) : 0;
         n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
       }
-      int incl = n;
+      const int mine = cut.units(n);
+      int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
       }
-      const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > w.g);
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > target);
       if (past) {
-        const int at = __ffs(past) - 1;
+        const int at = __ffs(past) - 1, units = __shfl_sync(0xFFFFFFFFu, mine, at);
         w.b = b0 + at;
         w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
-        w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - w.nt) * p.c.Hkv;
+        w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - units) * p.c.Hkv;
         w.ctx = __shfl_sync(0xFFFFFFFFu, ctx, at);
         w.nd = __shfl_sync(0xFFFFFFFFu, nd, at);
+        if (cut.pieces) {  // piece x of head h's `units`, as even as they come
+          w.h = (unsigned)(target - w.base) / (unsigned)units;
+          const int x = target - w.base - w.h * units;
+          w.t0 = (int)((long long)x * w.nt / units);
+          w.t1 = (int)((long long)(x + 1) * w.nt / units);
+          w.g1 = 1;
+        } else {
+          w.g = target;
+          w.g1 = target + cut.per;  // the list's end comes first in the last share (below)
+        }
         break;
       }
       w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
+    }
+    if (!cut.pieces && w.g < w.g1) {
+      int rest = 0;  // tiles of the list
+      for (int b = lane; b < p.B; b += 32) rest += tiles_of(p, b);
+      w.g1 = min(w.g1, __reduce_add_sync(0xFFFFFFFFu, rest) * p.c.Hkv);
+    }
+    if (blockIdx.x == 0) {
+      for (int b = lane; b < p.B; b += 32) {
+        int c;
+        if (new_tokens(p, b, c) < 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
+      }
     }
     if (lane == 0) *start = w;
   }
@@ -878,10 +912,14 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ctx;
   const int nd = new_tokens(p, b, ctx), nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-  int before, total;
-  warp_prefix(p, b, before, total);
-  const unsigned per = run_length(p, total), s0 = before + h * nt;
-  const int first = s0 / per, n = nt > 0 ? (int)((s0 + nt - 1) / per) - first + 1 : 0;
+  const Cut cut = make_cut(p, lane < p.B ? tiles_of(p, lane) : 0);
+  int before = 0;  // units of the sequences before b
+  for (int i = lane; i < b; i += 32) before += cut.units(tiles_of(p, i));
+  before = __reduce_add_sync(0xFFFFFFFFu, before) * p.c.Hkv;
+  // the segment's first block and their number
+  const int units = cut.units(nt), s0 = before + h * units;
+  const int first = cut.pieces ? s0 : s0 / cut.per;
+  const int n = cut.pieces ? units : nt > 0 ? (s0 + nt - 1) / cut.per - first + 1 : 0;
   wait_prerequisite();  // every block: the launches that follow rely on this one being over last
   if (rg * nr + r >= nd * p.group || n <= 1) return;
   auto part_of = [&](int i) {
