@@ -43,11 +43,11 @@ __device__ __forceinline__ long long pool_row(const KvView& c, int b, int h, lon
 template <int L>
 __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& exp_byte) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t top = 0;  // max |x| as ordered bf16 bits
+  // max |x| as ordered bf16 bits, two elements a word
+  uint32_t two = __vimax3_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  for (int o = L / 2; o > 0; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xFFFFFFFFu, two, o));
+  const uint32_t top = max(two & 0xffffu, two >> 16);
   const int ex = (int)(top >> 7);                       // biased exponent
   const int up = (top & 0x7fu) > 0x60u;                 // mantissa above 1.75 (448 = 1.75 * 2^8)
   const int e = top == 0 ? 0 : max(ex - 135 + up, -80);
@@ -60,8 +60,8 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& exp_byte)
     uint32_t v = 0;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint32_t two = w[2 * i + q];
-      const float2 f = make_float2(__uint_as_float(two << 16) * s, __uint_as_float(two & 0xffff0000u) * s);
+      const uint32_t x = w[2 * i + q];
+      const float2 f = make_float2(__uint_as_float(x << 16) * s, __uint_as_float(x & 0xffff0000u) * s);
       v |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * q);
     }
     out[i] = bad ? 0x7f7f7f7fu : v;
@@ -99,22 +99,31 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
   const int start = __ldg(p.start + b);
   const __nv_bfloat16* kb = p.k + b * p.ksb + h * p.ksh + lane * 8;
   const __nv_bfloat16* vb = p.v + b * p.vsb + h * p.vsh + lane * 8;
+  // lane u of a group finds out where its row u comes from and goes to
+  int my_src = -1;
+  long long my_dst = -1;
+  if (lane < kUnroll) {
+    const int n = n0 + lane * kRows;
+    if (n < count) {
+      my_src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
+      if (my_src < 0 || my_src >= p.M) {
+        report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
+        my_src = -1;
+      } else {
+        my_dst = pool_row(p.c, b, h, start < 0 ? -1ll : (long long)start + n, p.status, 102);
+      }
+    }
+  }
   uint4 rk[kUnroll], rv[kUnroll];
   long long dst[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int n = n0 + u * kRows;
-    dst[u] = -1;
+    const int src = __shfl_sync(0xFFFFFFFFu, my_src, u, L);
+    dst[u] = __shfl_sync(0xFFFFFFFFu, my_dst, u, L);
     rk[u] = rv[u] = make_uint4(0, 0, 0, 0);
-    if (n < count) {
-      const int src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
-      if (src < 0 || src >= p.M) {
-        report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
-      } else {
-        dst[u] = pool_row(p.c, b, h, start < 0 ? -1ll : (long long)start + n, p.status, 102);
-        rk[u] = __ldg(reinterpret_cast<const uint4*>(kb + src * p.ksn));
-        rv[u] = __ldg(reinterpret_cast<const uint4*>(vb + src * p.vsn));
-      }
+    if (src >= 0) {
+      rk[u] = __ldg(reinterpret_cast<const uint4*>(kb + src * p.ksn));
+      rv[u] = __ldg(reinterpret_cast<const uint4*>(vb + src * p.vsn));
     }
   }
 #pragma unroll
@@ -146,24 +155,31 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p,
   const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
   using Raw = typename std::conditional<F8, uint2, uint4>::type;
   const int len = min(__ldg(p.lens + b), p.N);
+  // lane u of a group finds its row u, and reads that row's exponents
+  long long my_row = -1;
+  uint32_t my_exp = 127 | 127 << 8;
+  if (lane < kUnroll && n0 + lane * kRows < len) {
+    my_row = pool_row(p.c, b, h, n0 + lane * kRows, p.status, 104);
+    if (F8 && my_row >= 0) my_exp = __ldg(p.c.ke + my_row) | (uint32_t)__ldg(p.c.ve + my_row) << 8;
+  }
   Raw rk[kUnroll], rv[kUnroll];
   uint32_t ek[kUnroll], ev[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int n = n0 + u * kRows;
+    const long long row = __shfl_sync(0xFFFFFFFFu, my_row, u, L);
     rk[u] = rv[u] = Raw{};
-    ek[u] = ev[u] = 127;
-    if (n < len) {
-      const long long row = pool_row(p.c, b, h, n, p.status, 104);
-      if (row >= 0) {
-        constexpr int kEl = F8 ? 1 : 2;
-        rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
-        rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
-        if constexpr (F8) {
-          ek[u] = __ldg(p.c.ke + row);
-          ev[u] = __ldg(p.c.ve + row);
-        }
-      }
+    if (row >= 0) {
+      constexpr int kEl = F8 ? 1 : 2;
+      rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
+      rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
+    }
+  }
+  if constexpr (F8) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t e = __shfl_sync(0xFFFFFFFFu, my_exp, u, L);
+      ek[u] = e & 0xffu;
+      ev[u] = e >> 8;
     }
   }
 #pragma unroll

@@ -21,115 +21,119 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows a lane group has in flight
 
+__device__ __forceinline__ float2 halves(uint32_t two) {  // of a bf16 pair
+  return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+
 // A row takes D / 8 lanes of eight elements (one 16-byte load each).  A lane
 // group takes `hb` consecutive heads of one token: its lanes form the cosines
-// and sines of their own eight elements once and keep them in registers for all
-// of those heads.  Bound by memory: each row is read and written once.
+// and sines of their own eight elements once, for all of those heads.
+//
+// Bound by memory (each row is read and written once) as long as few
+// instructions go with a row: with the weights multiplied into the cosines and
+// sines of the query and then the key heads,
+//   y = inv * (x * (c w) + partner * (s w')),  inv = rsqrt(mean(x^2) + eps),
+// and the partner arrives by exchanging the rows as read, two elements a word.
 template <int D>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int hb, int chunks) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p, int hb, int chunks) {
   constexpr int L = D / 8;
   constexpr int kRows = kThreads / L;
+  __shared__ float2 angles[8][kThreads];  // (cos, sin) of each thread's elements, read by it alone
   const int lane = threadIdx.x % L;
   const long long item = (long long)blockIdx.x * kRows + threadIdx.x / L;
-  // groups without work follow the last one through the shuffles, and store nothing
-  const bool live = item < (long long)p.B * p.N * chunks;
-  const int at = (int)(live ? item : (long long)p.B * p.N * chunks - 1);
-  const int tok = at / chunks, h0 = (at % chunks) * hb;
+  if (item >= (long long)p.B * p.N * chunks) return;
+  const unsigned group = (L == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) - lane);  // the group's lanes of the warp
+  const int tok = (int)(item / chunks), h0 = (int)(item % chunks) * hb;
   const int b = tok / p.N, n = tok % p.N;
   const int turned = p.Hq + p.Hkv;
   const int h1 = min(h0 + hb, turned + (p.v ? p.Hkv : 0));
   const __nv_bfloat16* src = p.x + b * p.sb + n * p.sn + lane * 8;
 
-  // y = x * c + partner * s, the partner being element i +- rot / 2 (the same
-  // element of another lane) or 2i + 1 of 2i and the reverse
+  // the partner is element i +- rot / 2 (the same element of another lane), or
+  // 2i + 1 of 2i and the reverse
   const int hl = p.rot / 16;
   const bool turn = lane * 8 < p.rot, low = lane < hl;
-  const int from = ((threadIdx.x & 31) - lane) + (!turn || p.interleaved ? lane : low ? lane + hl : lane - hl);
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
-  }
-  if (turn && h0 < turned) {
+  const int from = !turn || p.interleaved ? lane : low ? lane + hl : lane - hl;  // of the group
+  if (h0 < turned) {
     const double pos = (double)(p.pos ? __ldg(p.pos + tok) : n) * 0.15915494309189533577;  // 1 / (2 pi)
     const int i0 = p.interleaved ? lane * 4 : (low ? lane : lane - hl) * 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (p.interleaved && (e & 1)) continue;
-      const double turns = pos * __ldg(p.inv_freq + i0 + (p.interleaved ? e / 2 : e));
-      sincospif(2.f * (float)(turns - rint(turns)), &s[e], &c[e]);
-      if (p.interleaved) {
-        c[e + 1] = c[e];
-        s[e + 1] = s[e];
-        s[e] = -s[e];
-      } else if (low) {
-        s[e] = -s[e];
+      float sn = 0.f, cs = 1.f;
+      if (turn && !(p.interleaved && (e & 1))) {
+        const double turns = pos * __ldg(p.inv_freq + i0 + (p.interleaved ? e / 2 : e));
+        sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
+        if (p.interleaved || low) sn = -sn;
+      } else if (turn) {
+        const float2 pair = angles[e - 1 + (e == 0)][threadIdx.x];
+        cs = pair.x;
+        sn = -pair.y;
       }
+      angles[e][threadIdx.x] = make_float2(cs, sn);
     }
   }
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (p.qw) wq = __ldg(reinterpret_cast<const uint4*>(p.qw) + lane);
-  if (p.kw) wk = __ldg(reinterpret_cast<const uint4*>(p.kw) + lane);
 
-  for (int h = h0; h < h0 + hb; h += kUnroll) {  // the same trip count in every group of a warp
-    uint4 raw[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (h + u < h1) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(h + u) * D));
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int hh = h + u;
-      const bool is_q = hh < p.Hq, is_k = !is_q && hh < turned;
-      float x[8];
-      const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&raw[u]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __bfloat1622float2(r2[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+  for (int kind = 0; kind < 3; ++kind) {  // query, key, value heads
+    const int first = kind == 0 ? 0 : kind == 1 ? p.Hq : turned, heads = kind == 0 ? p.Hq : p.Hkv;
+    const int ha = max(h0, first), hz = min(h1, first + heads);
+    if (ha >= hz) continue;
+    __nv_bfloat16* base = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    __nv_bfloat16* dst = base + (((long long)b * heads - first) * p.N + n) * D + lane * 8;  // + head * N * D
+    const __nv_bfloat16* w = kind == 0 ? p.qw : p.kw;
+    float c[8], s[8];
+    if (kind < 2) {
+      uint4 wr = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wo = wr;  // ones
+      if (w) {
+        wr = __ldg(reinterpret_cast<const uint4*>(w) + lane);
+        wo = __ldg(reinterpret_cast<const uint4*>(w) + from);
       }
-      if (p.qw || p.kw) {
-        float ss = 0.f;
+      const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&wr);
+      const uint32_t* o2 = reinterpret_cast<const uint32_t*>(&wo);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < 8; ++e) {
+        const float2 a = angles[e][threadIdx.x], own = halves(w2[e / 2]), other = halves(o2[e / 2]);
+        c[e] = a.x * (e & 1 ? own.y : own.x);
+        s[e] = a.y * ((e & 1) != (p.interleaved != 0) ? other.y : other.x);
+      }
+    }
+    for (int h = ha; h < hz; h += kUnroll) {
+      uint4 raw[kUnroll];
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-          const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-          const uint4 wr = is_q ? wq : wk;
-          const __nv_bfloat162* w2 = reinterpret_cast<const __nv_bfloat162*>(&wr);
+      for (int u = 0; u < kUnroll; ++u)
+        if (h + u < hz) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(h + u) * D));
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (h + u >= hz) break;
+        uint4 out = raw[u];
+        if (kind < 2) {
+          uint32_t* x2 = reinterpret_cast<uint32_t*>(&out);
+          float inv = 1.f;
+          if (w) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = halves(x2[e]);
+              ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+            }
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+            inv = rsqrtf(ss * (1.f / D) + p.eps);
+          }
+          uint32_t other[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(w2[e]);
-            x[2 * e] = x[2 * e] * inv * f.x;
-            x[2 * e + 1] = x[2 * e + 1] * inv * f.y;
+            other[e] = p.interleaved ? __byte_perm(x2[e], 0, 0x1032) : __shfl_sync(group, x2[e], from, L);
+            if (!turn) other[e] = 0;  // and not an infinite element times no sine
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = halves(x2[e]), o = halves(other[e]);
+            const float y0 = fmaf(f.x, c[2 * e], o.x * s[2 * e]), y1 = fmaf(f.y, c[2 * e + 1], o.y * s[2 * e + 1]);
+            x2[e] = pack_bf16x2(y0 * inv, y1 * inv);
           }
         }
+        *reinterpret_cast<uint4*>(dst + (long long)(h + u) * p.N * D) = out;
       }
-      if (p.rot) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = p.interleaved ? x[e ^ 1] : __shfl_sync(0xFFFFFFFFu, x[e], from);
-          y[e] = turn ? x[e] * c[e] + other * s[e] : x[e];  // an infinite partner stays out of unturned elements
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = y[e];
-      }
-      if (!live || hh >= h1) continue;
-      __nv_bfloat16* dst;
-      if (is_q) dst = p.q + (((long long)b * p.Hq + hh) * p.N + n) * D;
-      else if (is_k) dst = p.k + (((long long)b * p.Hkv + hh - p.Hq) * p.N + n) * D;
-      else dst = p.v + (((long long)b * p.Hkv + hh - turned) * p.N + n) * D;
-      if (is_q || is_k) {
-        uint32_t* o = reinterpret_cast<uint32_t*>(&raw[u]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-      }
-      reinterpret_cast<uint4*>(dst)[lane] = raw[u];
     }
   }
 }
