@@ -16,6 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cu", "attn.cu", "bs_select.cu", "estimate.cu", "estimate_tc.cu", "grid.cu", "index.cu", "kv_cache.cu",
            "noalloc.cu", "rope.cu", "selftest.cu", "serve_api.cu", "tree_attn.cu"]
 LIB = os.path.join(HERE, "libminf.so")
+BINDING = os.path.join(HERE, "_binding.so")   # Python binding of the serving entry points (binding.cpp)
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 
@@ -27,9 +28,9 @@ def nvcc_path() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "minf.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -61,7 +62,30 @@ def build(verbose: bool = False, force: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
+    _build_binding(verbose)
     return LIB
+
+
+def _build_binding(verbose: bool) -> None:
+    """The extension module, linked against libminf.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    tmp = BINDING + ".tmp"
+    inc = [f for d in ext.include_paths() + [os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
+                                             sysconfig.get_paths()["include"]] for f in ("-isystem", d)]
+    libs = [f for d in ext.library_paths() for f in ("-L", d)]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_binding",
+           *inc, os.path.join(CSRC, "binding.cpp"), "-o", tmp, *libs, "-L", HERE, "-l:libminf.so", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0 or verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -449,13 +449,24 @@ def minf_selftest_exp2(x, stream=None):
 
 
 # -------------------------------------------------------------------- serving
-# Entry points of include/minf.h's serving part.  Tensors are checked here
-# (type, shape, device, contiguity: a mismatch raises MinfError with "invalid
-# argument"), since the C ABI sees bare pointers.  A call runs on its tensors'
-# device, on that device's current stream unless `stream` says otherwise, and
-# allocates missing outputs there.
+# Entry points of include/minf.h's serving part, through the extension module
+# built from binding.cpp.  Mismatched tensors (type, shape, device, contiguity)
+# raise MinfError with "invalid argument".  A call runs on its tensors' device,
+# on that device's current stream unless `stream` says otherwise, and allocates
+# missing outputs there.
 E4M3 = torch.float8_e4m3fn
-_BF16, _I32, _I64, _F32, _F64 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float64
+_ext = None
+
+
+def _binding():
+    """The extension module; raises if it has not been built."""
+    global _ext
+    if _ext is None:
+        lib()
+        from . import _binding as module
+        module.set_error(MinfError)
+        _ext = module
+    return _ext
 
 
 def _need(ok, what):
@@ -463,46 +474,16 @@ def _need(ok, what):
         raise MinfError(what, 1)
 
 
-def _same(fn, name, t, shape, device, dtype=_I32):
-    """Refuses a tensor that is not dense, of this shape and type, on `device`."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
-        raise MinfError(f"{fn} ({name}: contiguous {dtype} {list(shape)} on {device})", 1)
-
-
-def _dense(fn, name, t, like, shape, dtype=_BF16):
-    """A dense tensor of the given shape on `like`'s device, or a new one."""
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    _same(fn, name, t, shape, like.device, dtype)
-    return t
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ws(fn, ws, make, *args):
-    """The caller's workspace, or a new one."""
-    if ws is None:
-        return make(*args)
-    if not (ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == args[-1]):
-        raise MinfError(f"{fn} (ws: contiguous uint8 on {args[-1]})", 1)
-    return ws
-
-
-def _launch(t, stream, call):
-    """call(raw stream) with t's device and the call's stream current, so that
-    outputs are allocated where they are written."""
-    _need(t.is_cuda, "serving call (tensors in device memory)")
-    dev = t.get_device()
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` current."""
     if stream is None:
-        if dev == torch._C._cuda_getDevice():
-            return call(torch._C._cuda_getCurrentRawStream(dev))
-        with torch.cuda.device(dev):
-            return call(torch._C._cuda_getCurrentRawStream(dev))
-    _need(stream.device_index == dev, "serving call (stream of the tensors' device)")
+        return fn(*args)
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return fn(*args)
 
 
 def status_workspace(device="cuda"):
@@ -536,7 +517,7 @@ class KVCache:
         self.n_pages, self.Hkv, self.page, self.d = k.shape
         self.device = k.device
         self._c = _KVCacheC(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), *k.shape, 1 if f8 else 0)
-        self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
 
     @staticmethod
     def empty(n_pages, Hkv, page, d, e4m3=False, device="cuda"):
@@ -553,95 +534,19 @@ def minf_qkv_norm_rope(qkv, Hq, Hkv, pos=None, inv_freq=None, q_weight=None, k_w
     """Projected rows qkv [B, N, (Hq + 2 Hkv) * d] (any batch and row strides that are multiples of 8) to
     q [B, Hq, N, d], k and v [B, Hkv, N, d] (v is None without `want_v`), with the heads' norm and rotation
     (see include/minf.h).  pos [B, N] int32, inv_freq [rot_dim / 2] float64, weights [d] bf16."""
-    fn = "minf_qkv_norm_rope"
-    _need(qkv.dtype is _BF16 and qkv.dim() == 3 and Hq > 0 and Hkv > 0 and qkv.shape[2] % (Hq + 2 * Hkv) == 0
-          and (qkv.stride(2) == 1 or qkv.shape[2] == 1), f"{fn} (qkv: bf16 [B, N, (Hq + 2 Hkv) * d])")
-    B, N, C = qkv.shape
-    sb, sn, _ = qkv.stride()
-    d, dev, rot = C // (Hq + 2 * Hkv), qkv.device, 0
-    if pos is not None:
-        _same(fn, "pos", pos, (B, N), dev)
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _same(fn, "inv_freq", inv_freq, (rot // 2,), dev, _F64)
-    if q_weight is not None:
-        _same(fn, "q_weight", q_weight, (d,), dev, _BF16)
-    if k_weight is not None:
-        _same(fn, "k_weight", k_weight, (d,), dev, _BF16)
-
-    def call(st):
-        oq = _dense(fn, "q", q, qkv, (B, Hq, N, d))
-        ok = _dense(fn, "k", k, qkv, (B, Hkv, N, d))
-        ov = _dense(fn, "v", v, qkv, (B, Hkv, N, d)) if want_v or v is not None else None
-        _check(fn, lib().minf_qkv_norm_rope(
-            qkv.data_ptr(), B, N, Hq, Hkv, d, sb if B > 1 else 0, sn if N > 1 else C, _ptr(pos),
-            _ptr(inv_freq), rot, 1 if interleaved else 0, _ptr(q_weight), _ptr(k_weight), eps, oq.data_ptr(),
-            ok.data_ptr(), _ptr(ov), st))
-        return oq, ok, ov
-
-    return _launch(qkv, stream, call)
-
-
-def _table(fn, cache, pages, B):
-    _need(pages.dim() == 2, f"{fn} (pages: [B, max_pages])")
-    mp = pages.shape[1]
-    _same(fn, "pages", pages, (B, mp), cache.device)
-    return mp
-
-
-def _strides(t):
-    """Batch, head and row strides; those of a single one do not matter."""
-    return _Strides(*(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride())))
-
-
-_Strides = ctypes.c_int64 * 3
+    return _on(stream, _binding().qkv_norm_rope, qkv, Hq, Hkv, pos, inv_freq, q_weight, k_weight, eps, interleaved,
+               want_v, q, k, v)
 
 
 def minf_kv_write(k, v, cache: KVCache, pages, start, count=None, rows=None, ws=None, stream=None):
     """Writes k, v [B, Hkv, M, d] (d contiguous, other strides multiples of 8) into the cache at positions
     start[b] + i, i < count[b] (see include/minf.h); with `rows` [B, N] position start[b] + i gets row rows[b, i]."""
-    fn = "minf_kv_write"
-    dev = cache.device
-    _need(k.dim() == 4 and k.shape == v.shape and k.dtype is _BF16 and v.dtype is _BF16 and k.device == dev
-          and v.device == dev and k.shape[1] == cache.Hkv and k.shape[3] == cache.d and k.stride(3) == 1
-          and v.stride(3) == 1, f"{fn} (k, v: bf16 [B, Hkv, M, d] of the cache's Hkv, d and device)")
-    B, _, M, _ = k.shape
-    mp = _table(fn, cache, pages, B)
-    _same(fn, "start", start, (B,), dev)
-    if count is not None:
-        _same(fn, "count", count, (B,), dev)
-    N = M
-    if rows is not None:
-        _need(rows.dim() == 2, f"{fn} (rows: [B, N])")
-        N = rows.shape[1]
-        _same(fn, "rows", rows, (B, N), dev)
-
-    def call(st):
-        w = _ws(fn, ws, status_workspace, dev)
-        _check(fn, lib().minf_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), B, N, M, _strides(k), _strides(v),
-                                       pages.data_ptr(), mp, start.data_ptr(), _ptr(count), _ptr(rows), w.data_ptr(),
-                                       w.numel(), st))
-
-    _launch(k, stream, call)
+    _on(stream, _binding().kv_write, k, v, cache._addr, cache.k, pages, start, count, rows, ws)
 
 
 def minf_kv_read(cache: KVCache, pages, lens, N, k=None, v=None, ws=None, stream=None):
     """Positions 0 .. N-1 of every sequence as dense bf16 k, v [B, Hkv, N, d], zeros from lens[b] on."""
-    fn = "minf_kv_read"
-    _need(pages.dim() == 2 and N >= 0, f"{fn} (pages: [B, max_pages], N >= 0)")
-    B, dev = pages.shape[0], cache.device
-    mp = _table(fn, cache, pages, B)
-    _same(fn, "lens", lens, (B,), dev)
-
-    def call(st):
-        ok = _dense(fn, "k", k, cache.k, (B, cache.Hkv, N, cache.d))
-        ov = _dense(fn, "v", v, cache.k, (B, cache.Hkv, N, cache.d))
-        w = _ws(fn, ws, status_workspace, dev)
-        _check(fn, lib().minf_kv_read(cache._ref, pages.data_ptr(), B, mp, lens.data_ptr(), N, ok.data_ptr(),
-                                      ov.data_ptr(), w.data_ptr(), w.numel(), st))
-        return ok, ov
-
-    return _launch(cache.k, stream, call)
+    return _on(stream, _binding().kv_read, cache._addr, cache.k, pages, lens, N, k, v, ws)
 
 
 def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=None, o=None, lse=None, want_lse=True,
@@ -649,26 +554,6 @@ def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=N
     """Attention of the newest tokens q [B, Hq, T, d] over the cache, which holds their keys and values behind the
     ctx_lens[b] context positions (see include/minf.h).  tree_mask [B, T] int64: bit u of word t lets token t see
     token u; None is a chain.  n_draft [B] int32: tokens of each sequence (None: T); rows behind them are not
-    written (a new `o` is not initialised there)."""
-    fn = "minf_tree_attn"
-    dev = cache.device
-    _need(q.dim() == 4 and q.dtype is _BF16 and q.is_contiguous() and q.device == dev and q.shape[3] == cache.d,
-          f"{fn} (q: contiguous bf16 [B, Hq, T, d] of the cache's d and device)")
-    B, Hq, T, d = q.shape
-    mp = _table(fn, cache, pages, B)
-    _same(fn, "ctx_lens", ctx_lens, (B,), dev)
-    if n_draft is not None:
-        _same(fn, "n_draft", n_draft, (B,), dev)
-    if tree_mask is not None:
-        _same(fn, "tree_mask", tree_mask, (B, T), dev, _I64)
-
-    def call(st):
-        oo = torch.empty_like(q) if o is None else _dense(fn, "o", o, q, (B, Hq, T, d))
-        ol = _dense(fn, "lse", lse, q, (B, Hq, T), _F32) if want_lse or lse is not None else None
-        w = _ws(fn, ws, tree_attn_workspace, B, Hq, cache.Hkv, T, d, dev)
-        _check(fn, lib().minf_tree_attn(cache._ref, q.data_ptr(), B, Hq, T, scale, pages.data_ptr(), mp,
-                                        ctx_lens.data_ptr(), _ptr(n_draft), _ptr(tree_mask), oo.data_ptr(), _ptr(ol),
-                                        w.data_ptr(), w.numel(), st))
-        return oo, ol
-
-    return _launch(q, stream, call)
+    written (a new `o` is not initialised there).  lse is None without `want_lse`."""
+    return _on(stream, _binding().tree_attn, q, cache._addr, cache.k, pages, ctx_lens, n_draft, tree_mask, o, lse,
+               want_lse, scale, ws)
