@@ -4,7 +4,9 @@ routes every query head to Vertical-Slash, Block-Sparse or A-shape ("MInference
 online, attention over the indices only).
 
 This module only sequences C-ABI calls and owns their buffers (allocated once,
-up front, so that a timed step launches kernels and nothing else).
+up front, so that a timed step launches kernels and nothing else).  The serving
+part (:class:`ServePlan`) goes from projected rows to attention outputs, for a
+prompt and then for single or drafted tokens, over a paged key-value cache.
 """
 from __future__ import annotations
 
@@ -228,3 +230,95 @@ def device_status(plan: LayerPlan):
             if code:
                 return code
     return 0
+
+
+# --------------------------------------------------------------------- serving
+@dataclass
+class ServePlan:
+    """One layer's serving state for a batch of w.B sequences: the pre-fill plan
+    of their prompts, the paged cache, and each sequence's length in it."""
+    plan: LayerPlan
+    cache: minf.KVCache
+    pages: torch.Tensor            # [B, max_pages]
+    lens: torch.Tensor             # [B] cached positions
+    rotation: dict                 # norm and rotation arguments of minf_qkv_norm_rope
+    bufs: dict = field(default_factory=dict)
+
+
+def make_serve_plan(w: Workload, max_len: int, page: int = 64, e4m3: bool = False, inv_freq=None, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, interleaved: bool = False, max_tokens: int = 1,
+                    device="cuda") -> ServePlan:
+    """A plan for prompts of exactly w.N tokens and up to ``max_len`` positions
+    per sequence, drafted tokens included, of which a step brings at most
+    ``max_tokens``."""
+    dev = torch.device(device)
+    if max_len < w.N or not 1 <= max_tokens <= 64:
+        raise ValueError("max_len must hold the prompt, and a step brings 1 to 64 tokens")
+    per = -(-max_len // page)
+    cache = minf.KVCache.empty(w.B * per, w.Hkv, page, w.d, e4m3, device=dev)
+    pages = torch.arange(w.B * per, dtype=torch.int32, device=dev).view(w.B, per)
+    sp = ServePlan(make_plan(w, dev), cache, pages, torch.zeros(w.B, dtype=torch.int32, device=dev),
+                   dict(inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved))
+    sp.bufs["ws_cache"] = minf.status_workspace(dev)
+    sp.bufs["ws_tree"] = minf.tree_attn_workspace(w.B, w.Hq, w.Hkv, max_tokens, w.d, dev)
+    return sp
+
+
+def serve_prompt(sp: ServePlan, qkv, o=None, lse=None, stream=None):
+    """The prompts' projected rows qkv [B, N, (Hq + 2 Hkv) * d] through the
+    sparse layer; their keys and values fill the cache from position 0.  Returns
+    the attention output [B, Hq, N, d]."""
+    w = sp.plan.w
+    q, k, v = minf.minf_qkv_norm_rope(qkv, w.Hq, w.Hkv, stream=stream, **sp.rotation)
+    if o is None:
+        o = torch.empty_like(q)
+    run_layer(sp.plan, q, k, v, o, lse, stream=stream)
+    with torch.cuda.stream(stream):
+        sp.lens.fill_(w.N)
+        minf.minf_kv_write(k, v, sp.cache, sp.pages, torch.zeros_like(sp.lens), ws=sp.bufs["ws_cache"])
+    return o
+
+
+def serve_tokens(sp: ServePlan, qkv, depth=None, tree_mask=None, n_draft=None, stream=None):
+    """One step of T new tokens per sequence, projected rows qkv [B, T, (Hq + 2
+    Hkv) * d]: a generated token (T = 1), a chain, or a drafted tree whose token t
+    lies ``depth[t]`` positions (int32 [T], default t) behind the cached ones and
+    sees the tokens of ``tree_mask`` (see minf_tree_attn).  The tokens' keys and
+    values are written behind the cached positions, which do not grow until
+    :func:`keep_tokens`.  Returns (o [B, Hq, T, d], lse, k, v)."""
+    w = sp.plan.w
+    B, T, _ = qkv.shape
+    with torch.cuda.stream(stream):
+        if depth is None:
+            depth = torch.arange(T, dtype=torch.int32, device=qkv.device)
+        pos = sp.lens[:, None] + depth[None]
+        q, k, v = minf.minf_qkv_norm_rope(qkv, w.Hq, w.Hkv, pos=pos, **sp.rotation)
+        minf.minf_kv_write(k, v, sp.cache, sp.pages, sp.lens, count=n_draft, ws=sp.bufs["ws_cache"])
+        o, lse = minf.minf_tree_attn(q, sp.cache, sp.pages, sp.lens, n_draft=n_draft, tree_mask=tree_mask,
+                                     ws=sp.bufs["ws_tree"])
+    return o, lse, k, v
+
+
+def keep_tokens(sp: ServePlan, k, v, count, rows=None, stream=None):
+    """Keeps ``count[b]`` tokens of the last step (int32 [B]): the first ones, or
+    those of ``rows`` [B, n] in its order (a drafted tree's accepted path, root
+    first), whose keys and values move to their final positions."""
+    with torch.cuda.stream(stream):
+        if rows is not None:
+            minf.minf_kv_write(k, v, sp.cache, sp.pages, sp.lens, count=count, rows=rows, ws=sp.bufs["ws_cache"])
+        sp.lens.add_(count)
+
+
+def cached_prefix(sp: ServePlan, N: int, stream=None):
+    """Dense K, V [B, Hkv, N, d] of the cached positions (zeros behind a
+    sequence's last), as the pre-fill calls read them."""
+    return minf.minf_kv_read(sp.cache, sp.pages, sp.lens, N, ws=sp.bufs["ws_cache"], stream=stream)
+
+
+def serve_status(sp: ServePlan):
+    """First device-side error code of the serving plan (0 = none)."""
+    for name in ("ws_cache", "ws_tree"):
+        code = minf.minf_get_device_status(sp.bufs[name])
+        if code:
+            return code
+    return device_status(sp.plan)

@@ -18,7 +18,8 @@ import numpy as np
 import pytest
 import torch
 
-from dynamic_sparse_attention_minf_b200 import minf
+from dynamic_sparse_attention_minf_b200 import layer, minf
+from dynamic_sparse_attention_minf_b200 import workloads as wl
 from oracle import serve_oracle as so
 
 pytestmark = pytest.mark.gpu
@@ -480,3 +481,116 @@ def test_read_back_prefix_feeds_pre_fill(e4m3):
     tol = 2 * (U * o2.double().abs() + (U + 2.0 ** -10) * a)
     assert ((o[:, :, N - T:].double() - o2.double()).abs() <= tol).all()
     assert ((lse[:, :, N - T:] - lse2).abs() <= 2.0 ** -10).all()
+
+
+# ------------------------------------------------------------------ all together
+@pytest.mark.parametrize("e4m3,stream", [(False, False), (True, True)])
+def test_prompt_then_tree_then_tokens(e4m3, stream):
+    """A layer served end to end: prompt rows through the pre-fill (window over all keys), a drafted tree, its
+    accepted path kept, a chain, a generated token.  Every step against the float64 form on the cached values of
+    the final sequence, whose positions carry the rotations of their final places."""
+    B, Hq, Hkv, N, d, T = 2, 4, 2, 256, 128, 9
+    w = wl.small(Hq=Hq, Hkv=Hkv, N=N, d=d, seed=3, patterns=[wl.PAT_A] * Hq, n_sink=0, n_local=N)
+    w.B = B
+    g = torch.Generator(device="cuda").manual_seed(5)
+    C = (Hq + 2 * Hkv) * d
+    f = 500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64, device="cuda") / d)
+    qw, kw = ((1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16) for _ in "qk")
+    sp = layer.make_serve_plan(w, N + 40, page=16, e4m3=e4m3, inv_freq=f, q_weight=qw, k_weight=kw, max_tokens=T)
+    perm = torch.randperm(sp.pages.numel(), generator=g, device="cuda").to(torch.int32)
+    sp.pages.copy_(perm.view_as(sp.pages))
+    rows = lambda n: torch.randn(B, n, C, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    st = torch.cuda.Stream() if stream else None
+    sync = torch.cuda.synchronize
+
+    x0 = rows(N)
+    sync()
+    o0 = layer.serve_prompt(sp, x0, stream=st)
+    sync()
+    # tree: 0 -> 1, 2; 1 -> 3, 4; 2 -> 5; 4 -> 6, 7; 5 -> 8
+    parent = [-1, 0, 0, 1, 1, 2, 4, 4, 5]
+    see, depth = np.zeros((T, T), bool), []
+    for t, p in enumerate(parent):
+        if p >= 0:
+            see[t] = see[p]
+        see[t, t] = True
+        depth.append(0 if p < 0 else depth[p] + 1)
+    x1 = rows(T)
+    mask = torch.tensor([words(see)] * B, dtype=torch.int64, device="cuda")
+    sync()
+    o1, l1, k1, v1 = layer.serve_tokens(sp, x1, depth=i32(depth), tree_mask=mask, stream=st)
+    path = [[0, 1, 4, 7], [0, 2, 5, 5]]           # sequence 1 keeps three
+    kept = [4, 3]
+    layer.keep_tokens(sp, k1, v1, i32(kept), rows=i32(path), stream=st)
+    x2 = rows(2)
+    sync()
+    o2, l2, k2, v2 = layer.serve_tokens(sp, x2, stream=st)
+    layer.keep_tokens(sp, k2, v2, i32([2, 2]), stream=st)
+    x3 = rows(1)
+    sync()
+    o3, l3, k3, v3 = layer.serve_tokens(sp, x3, stream=st)
+    layer.keep_tokens(sp, k3, v3, i32([1, 1]), stream=st)
+    sync()
+    assert layer.serve_status(sp) == 0
+    assert sp.lens.tolist() == [N + 7, N + 6]
+    kd, vd = layer.cached_prefix(sp, N + 8, stream=st)
+    sync()
+    assert (kd[0, :, N + 7:] == 0).all() and (vd[1, :, N + 6:] == 0).all()
+    # the cache holds what rotating the final sequence's rows at their places gives
+    for b in range(B):
+        xb = torch.cat([x0[b], x1[b, path[b][:kept[b]]], x2[b], x3[b]])[None].contiguous()
+        qb, kb, vb = minf.minf_qkv_norm_rope(xb, Hq, Hkv, inv_freq=f, q_weight=qw, k_weight=kw)
+        n = xb.shape[1]
+        if e4m3:
+            ref = minf.KVCache.empty(-(-n // 16), Hkv, 16, d, True)
+            table = torch.arange(-(-n // 16), dtype=torch.int32, device="cuda")[None]
+            minf.minf_kv_write(kb, vb, ref, table, i32([0]))
+            kb, vb = minf.minf_kv_read(ref, table, i32([n]), n)
+        assert torch.equal(kd[b, :, :n], kb[0]) and torch.equal(vd[b, :, :n], vb[0])
+        # prompt rows, on the unquantised keys and values
+        qn = f64(minf.minf_qkv_norm_rope(x0[b:b + 1], Hq, Hkv, inv_freq=f, q_weight=qw, k_weight=kw)[0])
+        kp, vp = (f64(t) for t in minf.minf_qkv_norm_rope(x0[b:b + 1], Hq, Hkv, inv_freq=f, q_weight=qw, k_weight=kw)[1:])
+        for h in range(Hq):
+            t0 = N - 3
+            O, _, _ = so.tree_attention(qn[0, h, t0:], kp[0, h // 2], vp[0, h // 2], t0, np.tril(np.ones((3, 3), bool)),
+                                        d ** -0.5)
+            assert np.abs(f64(o0)[b, h, t0:] - O).max() <= 2e-2
+        # steps 2 and 3, rows of the final sequence
+        Kn, Vn, Q = f64(kd)[b:b + 1], f64(vd)[b:b + 1], f64(qb)
+        at = N + kept[b]
+        check_tree(Q[:, :, at:at + 2], Kn, Vn, [at], [2], [np.tril(np.ones((2, 2), bool))], d ** -0.5, f64(o2)[b:b + 1],
+                   f64(l2)[b:b + 1], e4m3)
+        check_tree(Q[:, :, at + 2:at + 3], Kn, Vn, [at + 2], [1], [np.ones((1, 1), bool)], d ** -0.5, f64(o3)[b:b + 1],
+                   f64(l3)[b:b + 1], e4m3)
+        # the accepted path's rows of the tree step are those of a chain over the final sequence
+        for i in range(kept[b]):
+            check_tree(Q[:, :, N + i:N + i + 1], Kn, Vn, [N + i], [1], [np.ones((1, 1), bool)], d ** -0.5,
+                       f64(o1)[b:b + 1, :, path[b][i]:path[b][i] + 1], f64(l1)[b:b + 1, :, path[b][i]:path[b][i] + 1], e4m3)
+
+
+def test_withheld_tiles_time_out_and_the_call_works_again():
+    """While the status block's hook is set, the first block loads no tiles: its bounded waits run out, the call
+    returns, and the status says so; afterwards the same workspace serves again."""
+    r = run_tree(8, 1, 4, 2, 128, 3, [700], [3], 64, True, "chain")
+    ws = r["ws"]
+    ws[24:28].view(torch.int32).fill_(1)
+    minf.minf_tree_attn(r["q"], r["c"], r["pages"], r["ctx"], ws=ws)
+    assert minf.minf_get_device_status(ws) == 5
+    ws[24:28].view(torch.int32).fill_(0)
+    o, lse = minf.minf_tree_attn(r["q"], r["c"], r["pages"], r["ctx"], ws=ws)
+    assert minf.minf_get_device_status(ws) == 0
+    assert torch.equal(o, r["o"]) and torch.equal(lse, r["lse"])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_tree_attention_many_sequences(e4m3):
+    """More sequences and heads than blocks (runs over several sequences), with empty ones among them, and a
+    batch beyond one warp's look at the lengths."""
+    rng = np.random.default_rng(4)
+    B = 75
+    ctx = rng.integers(0, 420, B)
+    nd = rng.integers(0, 3, B)
+    run_tree(11, B, 6, 3, 64, 2, ctx, nd, 16, e4m3, "chain")
+    ctx = np.zeros(40, int)
+    ctx[7] = 3000                                              # one long sequence among tiny ones
+    run_tree(12, 40, 2, 1, 128, 2, ctx, np.full(40, 2), 32, e4m3, "chain")
