@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cu", "attn.cu", "bs_select.cu", "estimate.cu", "estimate_tc.cu", "grid.cu", "index.cu", "kv_cache.cu",
-           "noalloc.cu", "rope.cu", "selftest.cu", "serve_api.cu", "tree_attn.cu"]
+           "noalloc.cu", "rope.cu", "selftest.cu", "serve_api.cu", "tree_attn.cu", "tree_wide.cu"]
 LIB = os.path.join(HERE, "libminf.so")
 BINDING = os.path.join(HERE, "_binding.so")   # Python binding of the serving entry points (binding.cpp)
 BUILD_DIR = os.path.join(ROOT, "_build")

@@ -60,9 +60,20 @@ __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint
       : "memory");
 }
 
-// Instruction descriptor of kind::f8f6f4 with fp32 D; A is e4m3, B e4m3 or e5m2.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int b_e5m2, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+// D(tmem) (+)= A(tmem) * B(smem), kind::f8f6f4 (A: four elements of a row in each 32-bit column).
+__device__ __forceinline__ void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with fp32 D; A and B are e4m3 or e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_e5m2, int b_e5m2, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 

@@ -79,5 +79,8 @@ bool tree_rows_supported(int Hq, int Hkv, int T);
 // bytes (64 with rows of 64 bytes), swizzled over that width.
 cudaError_t tree_attn_launch(int d, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                              cudaStream_t stream);
+// The blocks' part of it for groups of 128 rows (tree_wide.cu).
+cudaError_t tree_wide_launch(int d, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                             cudaStream_t stream);
 
 }  // namespace minf

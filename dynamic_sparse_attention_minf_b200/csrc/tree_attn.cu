@@ -12,7 +12,7 @@
 // keep loads in flight.
 //  * The products run transposed on the tensor cores, S^T = K Q^T and O^T =
 //    V^T P: the 128 keys of a tile (then the d elements of a value) are the 128
-//    rows of the instruction, and the query rows are its N = 16 .. 128 columns,
+//    rows of the instruction, and the query rows are its N = 16 .. 64 columns,
 //    so that one row costs 16 columns, not 128.  K and V tiles are used as TMA
 //    lays them down, in either element type.
 //  * A softmax thread owns a key: it sees the key's scores with every row, so a
@@ -33,95 +33,17 @@
 //    tiles, cut into equal runs, so that a ragged batch loads every block alike.
 //    What covers part of a sequence leaves its sums in the workspace, and a second
 //    kernel, launched ahead of time, joins them in order.
+// More than 64 rows of a KV head are tree_wide.cu's.
 #include <cuda_fp8.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "serve_device.cuh"
-#include "serve_internal.h"
+#include "tree_attn.cuh"
 
 namespace minf {
 
 namespace {
-
-constexpr int kMaxBlocks = 148;  // one block per SM
-constexpr float kFloor = -1e30f; // reference of a row that has seen nothing
-
-// ------------------------------------------------------------------ partition
-__device__ __forceinline__ int new_tokens(const TreeParams& p, int b, int& ctx) {
-  ctx = __ldg(p.ctx + b);
-  const int nd = p.ndraft ? __ldg(p.ndraft + b) : p.T;
-  const bool ok = ctx >= 0 && nd >= 0 && nd <= p.T && (long long)ctx + nd <= ((long long)p.c.max_pages << p.c.log_page);
-  return ok ? nd : -1;
-}
-// 128-key tiles of one KV head of sequence b (0: no new tokens, or bad lengths)
-__device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
-  int ctx;
-  const int nd = new_tokens(p, b, ctx);
-  return nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-}
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (unsigned)(a + b - 1) / (unsigned)b; }
-
-// How the work is cut, for a whole warp: in runs of `per` tiles of the list
-// (sequence-major, then KV head, then tile), or, with at most one sequence and
-// head per block, each of these into pieces of at most `per` tiles.  `units` of
-// a sequence's head are its tiles or its pieces.
-struct Cut {
-  int per;
-  bool pieces;
-  __device__ __forceinline__ int units(int nt) const { return pieces ? ceil_div(nt, per) : nt; }
-};
-// n0: tiles of sequence `lane` (read by the caller)
-__device__ __forceinline__ Cut make_cut(const TreeParams& p, int n0) {
-  const int lane = threadIdx.x & 31;
-  int total = n0, live = n0 > 0;
-  for (int b = lane + 32; b < p.B; b += 32) {
-    const int n = tiles_of(p, b);
-    total += n;
-    live += n > 0;
-  }
-  total = __reduce_add_sync(0xFFFFFFFFu, total) * p.c.Hkv;
-  live = __reduce_add_sync(0xFFFFFFFFu, live) * p.c.Hkv;
-  Cut c{max(1, ceil_div(total, p.lanes)), live <= p.lanes};
-  while (c.pieces) {  // longer pieces, by a sixteenth at least, until there is a block for each
-    int k = ceil_div(n0, c.per);
-    for (int b = lane + 32; b < p.B; b += 32) k += ceil_div(tiles_of(p, b), c.per);
-    k = __reduce_add_sync(0xFFFFFFFFu, k) * p.c.Hkv;
-    if (k <= p.lanes) break;
-    c.per = max(c.per + c.per / 16 + 1, (int)(((long long)c.per * k + p.lanes - 1) / p.lanes));
-  }
-  return c;
-}
-
-// A block's share, walked one (sequence, head) segment at a time; every role of
-// the block walks it by itself.
-struct Walk {
-  int g, g1, base;     // the run [g, g1) of the tile list; base: first tile of sequence b
-  int b, nt, ctx, nd;  // sequence b: tiles per head, context and new tokens
-  int h, t0, t1;       // the current segment: tiles [t0, t1) of KV head h
-  bool pieces;         // one segment only, set up already
-  __device__ __forceinline__ bool next(const TreeParams& p) {
-    if (g >= g1) return false;
-    if (pieces) {
-      g = g1;
-      return true;
-    }
-    while (g >= base + nt * p.c.Hkv) {
-      base += nt * p.c.Hkv;
-      ++b;
-      nd = new_tokens(p, b, ctx);
-      nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-    }
-    const unsigned x = g - base;
-    h = x / (unsigned)nt;
-    t0 = x - h * nt;
-    t1 = min(nt, t0 + (g1 - g));
-    g += t1 - t0;
-    return true;
-  }
-};
 
 // --------------------------------------------------------------------- layout
 template <int D, bool F8, int NR>
@@ -130,11 +52,7 @@ struct Cfg {
   // (one tile's chain of waits is longer than its loads), two otherwise
   static constexpr int kWG = NR == 16 || (NR == 32 && !F8) ? 4 : 2;
   static constexpr int kSoft = 128 * kWG;
-  // With 128 rows a softmax thread's sums alone take 128 registers: the fourth
-  // warp of the issuer and the producers idles, so that a whole warpgroup hands
-  // registers on (168 at launch; 208 and 88: 256 * 208 + 128 * 88 = 384 * 168).
-  static constexpr bool kSplitRegs = NR == 128;
-  static constexpr int kThreads = kSoft + (kSplitRegs ? 128 : 96);  // and the issuer, the K and the V producer
+  static constexpr int kThreads = kSoft + 96;         // and the issuer, the K and the V producer
   static constexpr int kRowB = D * (F8 ? 1 : 2);       // bytes of a cached row
   static constexpr int kPitch = kRowB < 128 ? kRowB : 128;  // row pitch within a swizzled region
   static constexpr int kRegions = kRowB / kPitch;
@@ -174,8 +92,8 @@ struct Cfg {
   static constexpr int kSCols = kQStack * NR, kOCols = kPStack * NR;  // of a warpgroup
   static constexpr int kOffO = kWG * kSCols;                          // first column of O
   static constexpr int kTmem = kWG * (kSCols + kOCols) <= 128 ? 128 : kWG * (kSCols + kOCols) <= 256 ? 256 : 512;
-  static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, kSCols, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
-  static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, kOCols, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
+  static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, kSCols, 0, 0, 0, 0) : idesc_bf16(128, NR, 0, 0);
+  static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, kOCols, 0, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
   static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
@@ -208,11 +126,6 @@ __device__ __forceinline__ float lane_totals(float (&v)[N]) {
     }
   }
   return v[0];
-}
-
-template <bool kOn>
-__device__ __forceinline__ void fewer_registers() {
-  if constexpr (kOn) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
 }
 
 template <int D, bool F8, int NR>
@@ -267,59 +180,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
       prefetch_tmap(&tmV);
     }
   } else if (warp == 0) {
-    // this block's share, and the sequence that it begins in (lane i looks at
-    // sequences i, i + 32, ...; a batch of up to 32 is read once)
-    int ctx = 0, nd = lane < p.B ? new_tokens(p, lane, ctx) : 0;
-    int n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-    const Cut cut = make_cut(p, n);
-    const int target = part_lane * (cut.pieces ? 1 : cut.per);  // first unit of the share
-    Walk w{};
-    w.pieces = cut.pieces;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      if (b0 > 0) {
-        nd = b0 + lane < p.B ? new_tokens(p, b0 + lane, ctx) : 0;
-        n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-      }
-      const int mine = cut.units(n);
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      const unsigned past = __ballot_sync(0xFFFFFFFFu, w.base + incl * p.c.Hkv > target);
-      if (past) {
-        const int at = __ffs(past) - 1, units = __shfl_sync(0xFFFFFFFFu, mine, at);
-        w.b = b0 + at;
-        w.nt = __shfl_sync(0xFFFFFFFFu, n, at);
-        w.base += (__shfl_sync(0xFFFFFFFFu, incl, at) - units) * p.c.Hkv;
-        w.ctx = __shfl_sync(0xFFFFFFFFu, ctx, at);
-        w.nd = __shfl_sync(0xFFFFFFFFu, nd, at);
-        if (cut.pieces) {  // piece x of head h's `units`, as even as they come
-          w.h = (unsigned)(target - w.base) / (unsigned)units;
-          const int x = target - w.base - w.h * units;
-          w.t0 = (int)((long long)x * w.nt / units);
-          w.t1 = (int)((long long)(x + 1) * w.nt / units);
-          w.g1 = 1;
-        } else {
-          w.g = target;
-          w.g1 = target + cut.per;  // the list's end comes first in the last share (below)
-        }
-        break;
-      }
-      w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
-    }
-    if (!cut.pieces && w.g < w.g1) {
-      int rest = 0;  // tiles of the list
-      for (int b = lane; b < p.B; b += 32) rest += tiles_of(p, b);
-      w.g1 = min(w.g1, __reduce_add_sync(0xFFFFFFFFu, rest) * p.c.Hkv);
-    }
-    if (blockIdx.x == 0) {
-      for (int b = lane; b < p.B; b += 32) {
-        int c;
-        if (new_tokens(p, b, c) < 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
-      }
-    }
+    const Walk w = block_share(p, part_lane);
     if (lane == 0) *start = w;
   }
   tc_fence_before();
@@ -330,81 +191,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
   Walk w = *start;
   __syncthreads();  // the run's place is the P buffer
 
-  if (warp > kLoadV) {
-    fewer_registers<C::kSplitRegs>();
-  } else if (warp == kLoadK || warp == kLoadV) {
+  if (warp == kLoadK || warp == kLoadV) {
     // ----------------------------------------------------------- producers
-    // One warp loads the K tiles and one the V tiles, each tile page by page
-    // (lane i < pages loads page i): a box costs its warp about 100 cycles to
-    // issue, and with pages of 16 rows a tile has 8 or 16 boxes of each.  With K
-    // go, in 8 bits, the exponents of the tile's keys and values, four keys per
-    // lane.  No load is waited for: page ids come 32 at a time, a batch ahead.
-    fewer_registers<C::kSplitRegs>();
     const bool is_k = warp == kLoadK;
-    const int stages = is_k ? C::kKStages : C::kVStages;
-    uint64_t* full = is_k ? k_full : v_full;
-    uint64_t* empty = is_k ? k_empty : v_empty;
-    uint8_t* ring = smem + (is_k ? C::kOffK : C::kOffV);
-    const CUtensorMap* map = is_k ? &tmK : &tmV;
-    int n = 0;
-    // failure-detection test hook: the first block withholds its key tiles, so its
-    // bounded waits run out and the call reports a timeout
-    bool live = p.status->withhold == 0 || blockIdx.x != 0;
-    while (live && w.next(p)) {
-      if (rg * NR >= w.nd * p.group) continue;
-      const int len = w.ctx + w.nd;
-      const int log = p.c.log_page, per_tile = 128 >> log, per_batch = 32 / per_tile;
-      const int first = w.t0 * per_tile, end = min(w.t1 * per_tile, (len + (1 << log) - 1) >> log);  // pages
-      const int32_t* table = p.c.pages + (long long)w.b * p.c.max_pages;
-      auto fetch = [&](int pg) { return pg + lane < end ? __ldg(table + pg + lane) : 0; };
-      int row = 0, ids = fetch(first);  // first pool row of this lane's page of the batch; the next batch
-      for (int t = w.t0; t < w.t1; ++t, ++n) {
-        const int at = (t - w.t0) % per_batch * per_tile, pages = min(per_tile, end - t * per_tile);
-        if (at == 0) {
-          if (ids < 0 || ids >= p.c.n_pages) {  // reported, and page 0 read instead
-            report(p.status, MINF_ERR_DEVICE_BOUNDS, 111);
-            ids = 0;
-          }
-          row = (ids * p.c.Hkv + w.h) << log;
-          ids = fetch(t * per_tile + 32);
-        }
-        const int st = n % stages;
-        if (n >= stages)
-          mbar_wait_or_abort(&empty[st], ((n / stages) - 1) & 1, abort, p.status, is_k ? 113 : 114);
-        if (__any_sync(0xFFFFFFFFu, *abort)) {
-          live = false;
-          break;
-        }
-        if (F8 && is_k) {
-          const int pg = (4 * lane) >> log;
-          const int from = __shfl_sync(0xFFFFFFFFu, row, at + pg) + ((4 * lane) & ((1 << log) - 1));
-          if (pg < pages) {
-            const uint32_t e = smem_u32(smem + C::kOffExp + st * C::kExpB + lane * 4);
-            cp_async4(e, p.c.ke + from);
-            cp_async4(e + 128, p.c.ve + from);
-          }
-          cp_async_mbar_arrive(&full[st]);
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (pages << log) * C::kRowB);
-        const int from = __shfl_sync(0xFFFFFFFFu, row, (at + lane) & 31);
-        if (lane < pages) {
-          uint8_t* dst = ring + st * C::kTileB + (lane << log) * C::kPitch;
-#pragma unroll
-          for (int r = 0; r < C::kRegions; ++r) tma_load_2d(dst + r * C::kRegion, map, &full[st], r * 64, from);
-        }
-        __syncwarp();
-      }
-    }
-    if (lane == 0) {  // never exit with copies in flight
-      int dummy = 0;
-      for (int i = max(0, n - stages); i < n; ++i)
-        mbar_wait(&full[i % stages], (i / stages) & 1, &dummy, p.status, is_k ? 115 : 116);
-    }
-    __syncwarp();
+    load_tiles<C, F8, NR>(p, is_k ? tmK : tmV, is_k, smem, is_k ? k_full : v_full, is_k ? k_empty : v_empty, rg, w, abort);
   } else if (warp == kIssuer) {
     // --------------------------------------------------------- MMA issuer
-    fewer_registers<C::kSplitRegs>();
     // operand descriptors: a base per buffer, plus constants (the start-address
     // field holds address / 16 and never carries out)
     const uint64_t q0 = sdesc(smem_u32(smem + C::kOffQ), C::kSCols * 16, 128, 0);
@@ -500,7 +292,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     // ------------------------------------------------------------- softmax
     // A failed wait is not followed up here: the status word and *abort are set,
     // every later wait ends at once, and the barriers below keep their counts.
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int wg = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lanes + wg * C::kSCols, o_col = lanes + C::kOffO + wg * C::kOCols;
@@ -973,22 +764,30 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
 int rows_per_block(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 template <int D, bool F8, int NR>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, cudaStream_t stream) {
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   using C = Cfg<D, F8, NR>;
-  const long long rows = (long long)p.T * p.group;
-  p.groups = (int)((rows + NR - 1) / NR);
-  p.rows = NR;
-  const long long most = (((long long)p.c.max_pages << p.c.log_page) + 127) / 128 * p.B * p.c.Hkv;
-  p.lanes = (int)std::min<long long>(kMaxBlocks / p.groups, most);
-  const long long bh = (long long)p.B * p.c.Hkv;
-  if (p.groups > kMaxBlocks || bh > 65535 || most >= (1ll << 30)) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   tree_attn_kernel<D, F8, NR><<<p.lanes * p.groups, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+template <int D, bool F8>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, cudaStream_t stream) {
+  const long long rows = (long long)p.T * p.group, bh = (long long)p.B * p.c.Hkv;
+  const long long most = (((long long)p.c.max_pages << p.c.log_page) + 127) / 128 * bh;  // tiles
+  p.rows = rows_per_block(rows);
+  p.groups = (int)((rows + p.rows - 1) / p.rows);
+  if (p.groups > kMaxBlocks || bh > 65535 || most >= (1ll << 30)) return cudaErrorInvalidConfiguration;
+  p.lanes = (int)std::min<long long>(kMaxBlocks / p.groups, most);
+  cudaError_t e = p.rows == 16   ? launch_rows<D, F8, 16>(tk, tv, p, stream)
+                  : p.rows == 32 ? launch_rows<D, F8, 32>(tk, tv, p, stream)
+                  : p.rows == 64 ? launch_rows<D, F8, 64>(tk, tv, p, stream)
+                                 : tree_wide_launch(D, tk, tv, p, stream);
   if (e != cudaSuccess) return e;
+  const int nr = (int)std::min<long long>(p.rows, rows);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.groups * std::min<long long>(NR, rows)), (unsigned)bh);
+  cfg.gridDim = dim3((unsigned)(p.groups * nr), (unsigned)bh);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
@@ -996,17 +795,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, c
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p, (int)std::min<long long>(NR, rows));
-}
-
-template <int D, bool F8>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  switch (rows_per_block((long long)p.T * p.group)) {
-    case 16: return launch<D, F8, 16>(tk, tv, p, stream);
-    case 32: return launch<D, F8, 32>(tk, tv, p, stream);
-    case 64: return launch<D, F8, 64>(tk, tv, p, stream);
-    default: return launch<D, F8, 128>(tk, tv, p, stream);
-  }
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p, nr);
 }
 
 }  // namespace
@@ -1022,8 +811,8 @@ bool tree_rows_supported(int Hq, int Hkv, int T) {
 
 cudaError_t tree_attn_launch(int d, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                              cudaStream_t stream) {
-  if (d == 128) return p.c.ke ? launch_rows<128, true>(tk, tv, p, stream) : launch_rows<128, false>(tk, tv, p, stream);
-  if (d == 64) return p.c.ke ? launch_rows<64, true>(tk, tv, p, stream) : launch_rows<64, false>(tk, tv, p, stream);
+  if (d == 128) return p.c.ke ? launch<128, true>(tk, tv, p, stream) : launch<128, false>(tk, tv, p, stream);
+  if (d == 64) return p.c.ke ? launch<64, true>(tk, tv, p, stream) : launch<64, false>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 
