@@ -97,7 +97,7 @@ struct Cfg {
   static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
-  static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 16.f;
+  static constexpr float kOff = F8 ? 8.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(24 * NR <= kPB && 4 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
@@ -414,19 +414,18 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         }
         mbar_wait_or_abort(&s_full[wg], uses & 1, abort, p.status, 123);
         tc_fence_after();
-        // scores of rows c0 .. of the thread's key
-        auto scores = [&](int c0, auto& s) {
+        // scores of rows c0 .. of the thread's key: asked for, and taken
+        auto ask = [&](int c0, auto& s, auto& lo) {
           tmem_ld(s_col + c0, s);
+          if constexpr (C::kQStack > 1) tmem_ld(s_col + NR + c0, lo);
+        };
+        auto take = [&](auto& s, auto& lo) {
+          tmem_landed(s);
           if constexpr (C::kQStack > 1) {
-            typename std::remove_reference<decltype(s)>::type lo;
-            tmem_ld(s_col + NR + c0, lo);
-            tmem_landed(s);
             tmem_landed(lo);
 #pragma unroll
             for (int c = 0; c < (int)(sizeof(s) / 4); ++c)
               s[c] = __float_as_uint(__uint_as_float(s[c]) + __uint_as_float(lo[c]));
-          } else {
-            tmem_landed(s);
           }
         };
         // From the tile's scores s to the exponents of their weights, two rows at a
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         // see the key.
         auto exponent2 = [&](auto masked, uint32_t s0, uint32_t s1, int r, const float* minus, float& t0, float& t1) {
           const uint64_t s2 = f32x2_pack(__uint_as_float(s0), __uint_as_float(s1));
-          const float2 m = *reinterpret_cast<const float2*>(minus + r);
+          const float2 m = minus ? *reinterpret_cast<const float2*>(minus + r) : make_float2(0.f, 0.f);
           if constexpr (F8) {
             const float2 f = *reinterpret_cast<const float2*>(fac + r);
             f32x2_unpack(f32x2_fma(f32x2_mul(s2, f32x2_pack(km, km)), f32x2_pack(f.x, f.y),
@@ -451,9 +450,33 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         };
         auto tile = [&](auto masked) {
           bool move = first;
+          // (16-bit rows beyond 16: the registers of this way in cost every tile more
+          // than it gains, 102 against 94 us for 64 rows over 128K)
+          constexpr bool kQuick = (F8 || NR == 16) && !decltype(masked)::value;
+          const bool quick = kQuick && first;
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {
-            if (move) {
+            if (kQuick && first && pass == 0) {
+              // A segment's first tile, with every key in sight: a reference near the
+              // rows' maxima will do, the largest of one warp's 32 keys.  Each warp
+              // gives a quarter of the rows theirs.
+              constexpr int kQ = NR / 4, kLd = kQ < 8 ? kQ : 8;
+#pragma unroll 1
+              for (int c0 = (warp & 3) * kQ; c0 < (warp & 3) * kQ + kQ; c0 += kLd) {
+                uint32_t s[kLd], lo[kLd];
+                ask(c0, s, lo);
+                take(s, lo);
+#pragma unroll
+                for (int c = 0; c < kLd; c += 2) {
+                  float t0, t1;
+                  exponent2(masked, s[c], s[c + 1], c0 + c, nullptr, t0, t1);
+                  t0 = -fmaxf(warp_max(t0) - C::kOff, kFloor);
+                  t1 = -fmaxf(warp_max(t1) - C::kOff, kFloor);
+                  if (lane == 0) *reinterpret_cast<float2*>(nref + c0 + c) = make_float2(t0, t1);
+                }
+              }
+              named_bar_sync(bar_wg, 128);
+            } else if (move) {
               // move the references up to the largest scores seen; O^T and l follow
               if (!first) {
                 mbar_wait_or_abort(&pv_done[wg], (uses - 1) & 1, abort, p.status, 124);
@@ -464,8 +487,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
               named_bar_sync(bar_wg, 128);
 #pragma unroll 1
               for (int c0 = 0; c0 < NR; c0 += 8) {
-                uint32_t s[8];
-                scores(c0, s);
+                uint32_t s[8], lo[8];
+                ask(c0, s, lo);
+                take(s, lo);
                 float mine = 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; c += 2) {
@@ -492,7 +516,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                 }
               }
               named_bar_sync(bar_wg, 128);
-              if (!first) {
+              if (first) {
+                if constexpr (kQuick) {  // the first pass's sums
+#pragma unroll
+                  for (int r = 0; r < NR / 2; ++r) l[r] = 0ull;
+                }
+              } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < C::kOCols; c0 += 8) {
                   uint32_t o[8];
@@ -507,8 +536,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                 // again.  Below 2^-90 what was there before them does not count.
 #pragma unroll
                 for (int c0 = 0; c0 < NR; c0 += 16) {
-                  uint32_t s[16];
-                  scores(c0, s);
+                  uint32_t s[16], lo[16];
+                  ask(c0, s, lo);
+                  take(s, lo);
 #pragma unroll
                   for (int c = 0; c < 16; c += 2) {
                     const int r = c0 + c;
@@ -528,8 +558,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
             float top = -INFINITY;
 #pragma unroll
             for (int c0 = 0; c0 < NR; c0 += C::kCh) {
-              uint32_t s[C::kCh];
-              scores(c0, s);
+              uint32_t s[C::kCh], lo[C::kCh];
+              ask(c0, s, lo);
+              take(s, lo);
               constexpr int kStep = F8 ? 16 : 8;
 #pragma unroll
               for (int g = 0; g < C::kCh; g += kStep) {
@@ -578,8 +609,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                       make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
               }
             }
-            // the first tile's references are the largest scores themselves
-            if (first || pass == 1 || bar_and(bar_wg, 128, !(top > C::kTop))) break;
+            // a first tile's references from all of its keys are the largest scores
+            if ((first && !quick) || pass == 1 || bar_and(bar_wg, 128, !(top > C::kTop))) break;
             move = true;
           }
           if (decltype(masked)::value && !in) {
@@ -702,8 +733,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   const int rg = blockIdx.x / nr, r = blockIdx.x % nr;  // nr rows of each row group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ctx;
-  const int nd = new_tokens(p, b, ctx), nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-  const Cut cut = make_cut(p, lane < p.B ? tiles_of(p, lane) : 0);
+  const int nd = new_tokens(p, b, ctx), nt = tiles(ctx, nd);
+  int c0 = 0;
+  const int d0 = lane < p.B ? new_tokens(p, lane, c0) : 0;
+  const Cut cut = make_cut(p, c0, d0);
   int before = 0;  // units of the sequences before b
   for (int i = lane; i < b; i += 32) before += cut.units(tiles_of(p, i));
   before = __reduce_add_sync(0xFFFFFFFFu, before) * p.c.Hkv;

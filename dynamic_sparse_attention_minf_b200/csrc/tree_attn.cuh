@@ -18,10 +18,11 @@ __device__ __forceinline__ int new_tokens(const TreeParams& p, int b, int& ctx) 
   return ok ? nd : -1;
 }
 // 128-key tiles of one KV head of sequence b (0: no new tokens, or bad lengths)
+__device__ __forceinline__ int tiles(int ctx, int nd) { return nd > 0 ? (ctx + nd + 127) >> 7 : 0; }
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
   int ctx;
   const int nd = new_tokens(p, b, ctx);
-  return nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+  return tiles(ctx, nd);
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (unsigned)(a + b - 1) / (unsigned)b; }
@@ -31,28 +32,32 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (unsigned)(a + b 
 // head per block, each of these into pieces of at most `per` tiles.  `units` of
 // a sequence's head are its tiles or its pieces.
 struct Cut {
-  int per;
-  bool pieces;
+  int per, total;  // total: tiles of the list
+  bool pieces, bad;  // bad: a sequence has bad lengths (and counts as empty)
   __device__ __forceinline__ int units(int nt) const { return pieces ? ceil_div(nt, per) : nt; }
 };
-// n0: tiles of sequence `lane` (read by the caller)
-__device__ __forceinline__ Cut make_cut(const TreeParams& p, int n0) {
-  const int lane = threadIdx.x & 31;
+// ctx0, nd0: lengths of sequence `lane` (read by the caller; 0 without one)
+__device__ __forceinline__ Cut make_cut(const TreeParams& p, int ctx0, int nd0) {
+  const int lane = threadIdx.x & 31, n0 = tiles(ctx0, nd0);
   int total = n0, live = n0 > 0;
+  bool bad = nd0 < 0;
   for (int b = lane + 32; b < p.B; b += 32) {
-    const int n = tiles_of(p, b);
+    int ctx;
+    const int nd = new_tokens(p, b, ctx), n = tiles(ctx, nd);
     total += n;
     live += n > 0;
+    bad = bad || nd < 0;
   }
   total = __reduce_add_sync(0xFFFFFFFFu, total) * p.c.Hkv;
   live = __reduce_add_sync(0xFFFFFFFFu, live) * p.c.Hkv;
-  Cut c{max(1, ceil_div(total, p.lanes)), live <= p.lanes};
+  Cut c{max(1, ceil_div(total, p.lanes)), total, live <= p.lanes, (bool)__any_sync(0xFFFFFFFFu, bad)};
   while (c.pieces) {  // longer pieces, by a sixteenth at least, until there is a block for each
     int k = ceil_div(n0, c.per);
     for (int b = lane + 32; b < p.B; b += 32) k += ceil_div(tiles_of(p, b), c.per);
     k = __reduce_add_sync(0xFFFFFFFFu, k) * p.c.Hkv;
     if (k <= p.lanes) break;
-    c.per = max(c.per + c.per / 16 + 1, (int)(((long long)c.per * k + p.lanes - 1) / p.lanes));
+    // per * k is at most the list's 2^30 tiles and one piece of 2^24 more for each of 148
+    c.per = max(c.per + c.per / 16 + 1, (int)(((unsigned)c.per * (unsigned)k + p.lanes - 1) / (unsigned)p.lanes));
   }
   return c;
 }
@@ -74,7 +79,7 @@ struct Walk {
       base += nt * p.c.Hkv;
       ++b;
       nd = new_tokens(p, b, ctx);
-      nt = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+      nt = tiles(ctx, nd);
     }
     const unsigned x = g - base;
     h = x / (unsigned)nt;
@@ -90,15 +95,16 @@ struct Walk {
 __device__ __forceinline__ Walk block_share(const TreeParams& p, int part_lane) {
   const int lane = threadIdx.x & 31;
   int ctx = 0, nd = lane < p.B ? new_tokens(p, lane, ctx) : 0;
-  int n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
-  const Cut cut = make_cut(p, n);
+  int n = tiles(ctx, nd);
+  const Cut cut = make_cut(p, ctx, nd);
+  if (cut.bad && blockIdx.x == 0 && lane == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
   const int target = part_lane * (cut.pieces ? 1 : cut.per);  // first unit of the share
   Walk w{};
   w.pieces = cut.pieces;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     if (b0 > 0) {
       nd = b0 + lane < p.B ? new_tokens(p, b0 + lane, ctx) : 0;
-      n = nd > 0 ? (ctx + nd + 127) >> 7 : 0;
+      n = tiles(ctx, nd);
     }
     const int mine = cut.units(n);
     int incl = mine;
@@ -118,27 +124,16 @@ __device__ __forceinline__ Walk block_share(const TreeParams& p, int part_lane) 
       if (cut.pieces) {  // piece x of head h's `units`, as even as they come
         w.h = (unsigned)(target - w.base) / (unsigned)units;
         const int x = target - w.base - w.h * units;
-        w.t0 = (int)((long long)x * w.nt / units);
-        w.t1 = (int)((long long)(x + 1) * w.nt / units);
+        w.t0 = (unsigned)x * (unsigned)w.nt / (unsigned)units;  // at most 148 * 2^24
+        w.t1 = (unsigned)(x + 1) * (unsigned)w.nt / (unsigned)units;
         w.g1 = 1;
       } else {
         w.g = target;
-        w.g1 = target + cut.per;  // the list's end comes first in the last share (below)
+        w.g1 = min(target + cut.per, cut.total);
       }
       break;
     }
     w.base += __shfl_sync(0xFFFFFFFFu, incl, 31) * p.c.Hkv;
-  }
-  if (!cut.pieces && w.g < w.g1) {
-    int rest = 0;  // tiles of the list
-    for (int b = lane; b < p.B; b += 32) rest += tiles_of(p, b);
-    w.g1 = min(w.g1, __reduce_add_sync(0xFFFFFFFFu, rest) * p.c.Hkv);
-  }
-  if (blockIdx.x == 0) {
-    for (int b = lane; b < p.B; b += 32) {
-      int c;
-      if (new_tokens(p, b, c) < 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 110);
-    }
   }
   return w;
 }
