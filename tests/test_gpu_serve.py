@@ -594,3 +594,85 @@ def test_tree_attention_many_sequences(e4m3):
     ctx = np.zeros(40, int)
     ctx[7] = 3000                                              # one long sequence among tiny ones
     run_tree(12, 40, 2, 1, 128, 2, ctx, np.full(40, 2), 32, e4m3, "chain")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_offsets_beyond_32_bits(e4m3):
+    """Pages at the end of a pool of more than 4 GiB."""
+    Hkv, page, d, L = 2, 64, 128, 150
+    n = 140000 if not e4m3 else 270000                          # 4.6 / 4.4 GB of keys
+    c = minf.KVCache.empty(n, Hkv, page, d, e4m3)
+    pages = i32([[n - 1, n - 3, n - 2]])
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(1, Hkv, L, d, generator=g).to(torch.bfloat16).cuda() for _ in "kv")
+    q = torch.randn(1, 4, 2, d, generator=g).to(torch.bfloat16).cuda()
+    ws = minf.tree_attn_workspace(1, 4, Hkv, 2, d)
+    minf.minf_kv_write(k, v, c, pages, i32([0]), ws=ws)
+    kd, vd = minf.minf_kv_read(c, pages, i32([L]), L, ws=ws)
+    if not e4m3:
+        assert torch.equal(kd, k) and torch.equal(vd, v)
+    o, lse = minf.minf_tree_attn(q, c, pages, i32([L - 2]), ws=ws)
+    assert minf.minf_get_device_status(ws) == 0
+    check_tree(f64(q), f64(kd), f64(vd), [L - 2], [2], [np.tril(np.ones((2, 2), bool))], d ** -0.5, f64(o), f64(lse), e4m3)
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_infinite_scores(T):
+    """A score of +infinity makes its rows NaN, wherever its key lies; -infinity weighs nothing."""
+    for at in (3, 290):
+        r = run_tree(21, 1, 4, 1, 64, T, [300], [T], 16, False, "chain")
+        k, v = minf.minf_kv_read(r["c"], r["pages"], i32([300 + T]), 300 + T)
+        k[0, 0, at] = 0
+        k[0, 0, at, 0] = float("inf")
+        q = r["q"].clone()
+        q[..., 0] = q[..., 0].abs() + 1
+        q[0, 0, :, 0] *= -1                                      # head 0: -infinity
+        minf.minf_kv_write(k, v, r["c"], r["pages"], i32([0]))
+        o, lse = minf.minf_tree_attn(q, r["c"], r["pages"], r["ctx"], ws=r["ws"])
+        assert torch.isnan(o[0, 1:]).all() and torch.isnan(lse[0, 1:]).all()
+        keep = [j for j in range(300 + T) if j != at]
+        see = np.tril(np.ones((T, T), bool))
+        O, L, A = so.tree_attention(f64(q)[0, 0], f64(k)[0, 0, keep], f64(v)[0, 0, keep], 299, see, 64 ** -0.5)
+        assert (np.abs(f64(o)[0, 0] - O) <= U * np.abs(O) + (U + 2.0 ** -10) * A).all()
+        assert np.abs(f64(lse)[0, 0] - L).max() <= 2.0 ** -10
+
+
+def test_wide_rows_time_out_and_work_again():
+    r = run_tree(31, 1, 8, 2, 128, 40, [700], [40], 64, True, "tree")
+    ws = r["ws"]
+    ws[24:28].view(torch.int32).fill_(1)
+    minf.minf_tree_attn(r["q"], r["c"], r["pages"], r["ctx"], tree_mask=r["tm"], ws=ws)
+    assert minf.minf_get_device_status(ws) == 5
+    ws[24:28].view(torch.int32).fill_(0)
+    o, lse = minf.minf_tree_attn(r["q"], r["c"], r["pages"], r["ctx"], tree_mask=r["tm"], ws=ws)
+    assert minf.minf_get_device_status(ws) == 0
+    assert torch.equal(o, r["o"]) and torch.equal(lse, r["lse"])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv", [(64, 4, 2), (64, 2, 2), (20, 4, 1), (32, 4, 1)])
+def test_wide_and_narrow_rows_late_maximum(T, Hq, Hkv, e4m3):
+    """64 to 128 rows: a key beyond all others late in the context, values of very different size, and several
+    blocks to a sequence; drafted keys fill the last tile."""
+    def spike(q, k, v):
+        k[:, :, 1400] = 5 * q[:, :Hkv, 3]
+        v[:, :, :1400] *= 1e-3
+    run_tree(T, 1, Hq, Hkv, 128, T, [128 * 14 - T], [T], 32, e4m3, "tree", spike=spike)
+    run_tree(T + 1, 2, Hq, Hkv, 64, T, [1200, 0], [T, 5], 16, e4m3, "random")
+
+
+def test_calls_on_two_streams_at_once():
+    """The same cache read by two streams, each with its own workspace."""
+    a = run_tree(41, 2, 8, 2, 128, 4, [3000, 1500], [4, 4], 64, True, "chain")
+    ws = [a["ws"], minf.tree_attn_workspace(2, 8, 2, 4, 128)]
+    ss = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s in (0, 1):
+            outs[s].append(minf.minf_tree_attn(a["q"], a["c"], a["pages"], a["ctx"], ws=ws[s], stream=ss[s]))
+    torch.cuda.synchronize()
+    for s in (0, 1):
+        assert minf.minf_get_device_status(ws[s]) == 0
+        for o, lse in outs[s]:
+            assert torch.equal(o, a["o"]) and torch.equal(lse, a["lse"])
