@@ -97,7 +97,7 @@ struct Cfg {
   static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
   // use the top of their range; a score kTop above the reference moves it
-  static constexpr float kOff = F8 ? 8.f : 0.f, kTop = F8 ? 15.f : 16.f;
+  static constexpr float kOff = F8 ? 4.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(24 * NR <= kPB && 4 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");

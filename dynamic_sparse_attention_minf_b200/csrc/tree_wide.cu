@@ -54,7 +54,7 @@ struct Wide {
   static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, 128, 0, 0, 0, 0) : idesc_bf16(128, 128, 0, 0);
   static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, D, 1, 0, 0, 1) : idesc_bf16(128, D, 0, 1);
   // the weights' reference lies kOff below the maximum seen; kTop above it, it moves
-  static constexpr float kOff = F8 ? 11.f : 0.f, kTop = F8 ? 15.f : 8.f;
+  static constexpr float kOff = F8 ? 4.f : 0.f, kTop = F8 ? 15.f : 8.f;
   static_assert(kVStages >= 2 && kKStages >= 2 && kSmem <= 232448, "shared memory");
 };
 
