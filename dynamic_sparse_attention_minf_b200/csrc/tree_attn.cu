@@ -452,17 +452,20 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
           bool move = first;
           // (16-bit rows beyond 16: the registers of this way in cost every tile more
           // than it gains, 102 against 94 us for 64 rows over 128K)
-          constexpr bool kQuick = (F8 || NR == 16) && !decltype(masked)::value;
-          const bool quick = kQuick && first;
+          constexpr bool kQuick = F8 || NR == 16;
+          const bool quick = kQuick && first && j0 < w.ctx;
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {
-            if (kQuick && first && pass == 0) {
-              // A segment's first tile, with every key in sight: a reference near the
-              // rows' maxima will do, the largest of one warp's 32 keys.  Each warp
-              // gives a quarter of the rows theirs.
+            if (quick && pass == 0) {
+              // A segment's first tile: a reference near the rows' maxima will do, the
+              // largest of one warp's 32 keys.  Each warp gives a quarter of the rows
+              // theirs; in a tile with drafted keys the first warp, which has keys of
+              // the context, gives all of them.
               constexpr int kQ = NR / 4, kLd = kQ < 8 ? kQ : 8;
+              const bool all = decltype(masked)::value;
+              const int ra = all ? 0 : (warp & 3) * kQ, rz = !all ? ra + kQ : (warp & 3) == 0 ? NR : 0;
 #pragma unroll 1
-              for (int c0 = (warp & 3) * kQ; c0 < (warp & 3) * kQ + kQ; c0 += kLd) {
+              for (int c0 = ra; c0 < rz; c0 += kLd) {
                 uint32_t s[kLd], lo[kLd];
                 ask(c0, s, lo);
                 take(s, lo);
