@@ -551,9 +551,15 @@ def run_kernel_case(args):
     the Grid-pattern attention of the 8 heads over ``--N`` / 256 frames of 256
     tokens (top-100 frame blocks), timed with CUDA events.  ``--kernel
     vs_est_layer`` times the Vertical-Slash estimation of all VS heads of the
-    ``--config`` layer at full size."""
+    ``--config`` layer at full size.  ``--kernel serve`` times the serving calls
+    on the layer's geometry (32 query / 8 KV heads, d = 128): rotation, cache
+    write and read of an ``--N``-token prompt, and the attention of ``--tokens``
+    new tokens over it."""
     from dynamic_sparse_attention_minf_b200 import layer, minf
     from dynamic_sparse_attention_minf_b200 import workloads as wl
+    if args.kernel == "serve":
+        _run_serve_case(args, minf, wl.config(WORKLOAD_ID, N=args.N))
+        return
     if args.kernel == "vs_est_layer":
         # Vertical-Slash estimation of every VS head of the --config layer at
         # its full size, 3 rounds of one untimed and 5 timed calls (CUDA events)
@@ -642,6 +648,48 @@ def run_kernel_case(args):
                       "tiles_per_launch": tiles, "kernel_sources_sha256": kernel_sources_digest()}))
 
 
+def _run_serve_case(args, minf, w):
+    N, T, d = args.N, args.tokens, w.d
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(w.seed)
+    rows = torch.randn(1, N, (w.Hq + 2 * w.Hkv) * d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    freq = 500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64, device="cuda") / d)
+    weight = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    page = 64
+    n = -(-(N + T) // page)
+    cache = minf.KVCache.empty(n, w.Hkv, page, d, args.e4m3)
+    pages = torch.randperm(n, generator=gen, device="cuda").to(torch.int32)[None].contiguous()
+    start, lens = torch.zeros(1, **i32), torch.full((1,), N, **i32)
+    ws, wt = minf.status_workspace(), minf.tree_attn_workspace(1, w.Hq, w.Hkv, T, d)
+    q, k, v = minf.minf_qkv_norm_rope(rows, w.Hq, w.Hkv, inv_freq=freq, q_weight=weight, k_weight=weight)
+    new = torch.randn(1, w.Hq, T, d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    minf.minf_kv_write(k[:, :, :T], v[:, :, :T], cache, pages, lens, ws=ws)
+    kd, vd = torch.empty_like(k), torch.empty_like(v)
+    o, lse = torch.empty_like(new), torch.empty(1, w.Hq, T, device="cuda")
+    kv_row = 2 * w.Hkv * (d + 1 if args.e4m3 else 2 * d)   # bytes of one cached position
+    calls = {
+        "qkv_norm_rope": (lambda: minf.minf_qkv_norm_rope(rows, w.Hq, w.Hkv, inv_freq=freq, q_weight=weight,
+                                                          k_weight=weight, q=q, k=k, v=v), 2 * rows.numel() * 2),
+        "kv_write": (lambda: minf.minf_kv_write(k, v, cache, pages, start, ws=ws), N * (kv_row + 4 * w.Hkv * d)),
+        "kv_read": (lambda: minf.minf_kv_read(cache, pages, lens, N, k=kd, v=vd, ws=ws), N * (kv_row + 4 * w.Hkv * d)),
+        "tree_attn": (lambda: minf.minf_tree_attn(new, cache, pages, lens, o=o, lse=lse, ws=wt), (N + T) * kv_row),
+    }
+    res = {}
+    for name, (fn, nbytes) in calls.items():
+        for _ in range(args.warmup):
+            fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / args.steps
+        res[name] = {"ms": ms, "gbs": nbytes / ms / 1e6}
+    print(json.dumps({"kernel": "serve", "N": N, "tokens": T, "cache": "e4m3" if args.e4m3 else "bf16", **res,
+                      "status": [minf.minf_get_device_status(x) for x in (ws, wt)]}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -654,10 +702,12 @@ def main():
     ap.add_argument("--config", type=int, default=WORKLOAD_ID, choices=[2, 3, 4],
                     help="workload: 4 (default) the 1M-token mixed layer, 2 the 128K mixed layer, "
                          "3 the 512K all-Vertical-Slash layer")
-    ap.add_argument("--kernel", choices=["dense", "vs", "vs_est", "bs_est", "grid", "vs_est_layer"], default=None,
+    ap.add_argument("--kernel", choices=["dense", "vs", "vs_est", "bs_est", "grid", "vs_est_layer", "serve"], default=None,
                     help="run only this kernel on a small case (for profiling); vs_est_layer times the "
                          "Vertical-Slash estimation of the --config layer's VS heads at full size")
     ap.add_argument("--N", type=int, default=262144, help="tokens of the --kernel case")
+    ap.add_argument("--tokens", type=int, default=1, help="new tokens of the serve case")
+    ap.add_argument("--e4m3", action="store_true", help="8-bit cache in the serve case")
     ap.add_argument("--shard", choices=["kv", "replicas"], default="kv",
                     help="with several GPUs: split one layer by KV-head group (default) or run a layer per rank")
     ap.add_argument("--clock-log", default=None,

@@ -32,7 +32,7 @@ struct Wide {
   static constexpr int kQParts = F8 ? 2 : 1, kPParts = F8 ? 3 : 1;
   static constexpr int kQPart = 128 * kRowB;
   static constexpr int kExpB = F8 ? 256 : 0;
-  static constexpr int kKeyB = F8 ? 2 * 128 * 16 : 0;  // per key of two tiles: 2^key, value exponent, 2^-value
+  static constexpr int kKeyB = F8 ? 2 * 3 * 512 : 0;  // of two tiles' keys: 2^key exponents, value exponents, 2^-those
   static constexpr int kTiles = (232448 - kQParts * kQPart - kKeyB - 8 * kExpB - 3072) / kTileB;
   static constexpr int kKStages = (kTiles + 1) / 2 < 8 ? (kTiles + 1) / 2 : 8;
   static constexpr int kVStages = kTiles / 2 < 8 ? kTiles / 2 : 8;
@@ -289,8 +289,9 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
         const int b = it & 1, kst = it % C::kKStages;
         const int j0 = (w.t0 + i) * 128 + wg * 64;  // first key of the half
         const uint32_t s_col = lanes + b * 128 + wg * 64;
-        // per key: (2^key exponent, value exponent, its inverse power)
-        float4* keys = reinterpret_cast<float4*>(smem + C::kOffKey) + b * 128 + wg * 64;
+        // the half's keys: 2^key exponent, value exponent, its inverse power (four keys a read)
+        float* key_pow = reinterpret_cast<float*>(smem + C::kOffKey) + b * 384 + wg * 64;
+        float *val_exp = key_pow + 128, *val_inv = key_pow + 256;
         if constexpr (F8) {
           if (tid < 64) {
             mbar_wait_or_abort(&k_full[kst], (it / C::kKStages) & 1, abort, p.status, 122);
@@ -298,13 +299,10 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
             const uint32_t ke = e[0], ve = e[128];
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_empty[kst]);
-            float4 k = make_float4(0.f, 0.f, 1.f, 0.f);
-            if (j0 + tid < len) {
-              k.x = ke == 255u ? NAN : __uint_as_float(ke << 23);
-              k.y = ve == 255u ? NAN : (float)((int)ve - 127);
-              k.z = ve == 255u ? NAN : __uint_as_float((254u - ve) << 23);
-            }
-            keys[tid] = k;
+            const bool in = j0 + tid < len;
+            key_pow[tid] = !in ? 0.f : ke == 255u ? NAN : __uint_as_float(ke << 23);
+            val_exp[tid] = !in ? 0.f : ve == 255u ? NAN : (float)((int)ve - 127);
+            val_inv[tid] = !in ? 1.f : ve == 255u ? NAN : __uint_as_float((254u - ve) << 23);
           }
           named_bar_sync(bar_wg, 128);
         }
@@ -318,15 +316,18 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
         // 8-bit: scores in powers of two with the values' exponents, in place
         if constexpr (F8) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float4 ka = keys[c], kb = keys[c + 1];
-            float y0, y1;
-            f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_pack(__uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1])),
-                                             f32x2_pack(ka.x, kb.x)),
-                                   mul2, f32x2_pack(ka.y, kb.y)),
-                         y0, y1);
-            s[c / 32][c % 32] = __float_as_uint(y0);
-            s[c / 32][c % 32 + 1] = __float_as_uint(y1);
+          for (int c = 0; c < 64; c += 4) {
+            const float4 k = *reinterpret_cast<const float4*>(key_pow + c), v = *reinterpret_cast<const float4*>(val_exp + c);
+            uint32_t* x = &s[c / 32][c % 32];
+            float y[4];
+            f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), f32x2_pack(k.x, k.y)),
+                                   mul2, f32x2_pack(v.x, v.y)),
+                         y[0], y[1]);
+            f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_pack(__uint_as_float(x[2]), __uint_as_float(x[3])), f32x2_pack(k.z, k.w)),
+                                   mul2, f32x2_pack(v.z, v.w)),
+                         y[2], y[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __float_as_uint(y[e]);
           }
         }
         const int base = j0 - w.ctx;  // drafted index of the half's first key
@@ -395,12 +396,12 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
               uint32_t x[2];
+              const float4 iv = *reinterpret_cast<const float4*>(val_inv + h * 32 + c);
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
                 float p0, p1;
                 weights2(s[h][c + 2 * g], s[h][c + 2 * g + 1], p0, p1);
-                sum[g] = f32x2_fma(f32x2_pack(p0, p1),
-                                   f32x2_pack(keys[h * 32 + c + 2 * g].z, keys[h * 32 + c + 2 * g + 1].z), sum[g]);
+                sum[g] = f32x2_fma(f32x2_pack(p0, p1), g == 0 ? f32x2_pack(iv.x, iv.y) : f32x2_pack(iv.z, iv.w), sum[g]);
                 const __half2 two = __floats2half2_rn(p0, p1);
                 x[g] = *reinterpret_cast<const uint32_t*>(&two);
               }
