@@ -270,10 +270,10 @@ def serve_prompt(sp: ServePlan, qkv, o=None, lse=None, stream=None):
     the attention output [B, Hq, N, d]."""
     w = sp.plan.w
     q, k, v = minf.minf_qkv_norm_rope(qkv, w.Hq, w.Hkv, stream=stream, **sp.rotation)
-    if o is None:
-        o = torch.empty_like(q)
-    run_layer(sp.plan, q, k, v, o, lse, stream=stream)
     with torch.cuda.stream(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        run_layer(sp.plan, q, k, v, o, lse, stream=stream)
         sp.lens.fill_(w.N)
         minf.minf_kv_write(k, v, sp.cache, sp.pages, torch.zeros_like(sp.lens), ws=sp.bufs["ws_cache"])
     return o

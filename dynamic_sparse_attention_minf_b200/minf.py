@@ -478,10 +478,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, fn, *args):
-    """fn(*args) with `stream` current."""
+def _on(stream, device, fn, *args):
+    """fn(*args) with `stream`, one of the tensors' device, current."""
     if stream is None:
         return fn(*args)
+    _need(stream.device == device, "serving call (stream of the tensors' device)")
     with torch.cuda.stream(stream):
         return fn(*args)
 
@@ -534,19 +535,19 @@ def minf_qkv_norm_rope(qkv, Hq, Hkv, pos=None, inv_freq=None, q_weight=None, k_w
     """Projected rows qkv [B, N, (Hq + 2 Hkv) * d] (any batch and row strides that are multiples of 8) to
     q [B, Hq, N, d], k and v [B, Hkv, N, d] (v is None without `want_v`), with the heads' norm and rotation
     (see include/minf.h).  pos [B, N] int32, inv_freq [rot_dim / 2] float64, weights [d] bf16."""
-    return _on(stream, _binding().qkv_norm_rope, qkv, Hq, Hkv, pos, inv_freq, q_weight, k_weight, eps, interleaved,
+    return _on(stream, qkv.device, _binding().qkv_norm_rope, qkv, Hq, Hkv, pos, inv_freq, q_weight, k_weight, eps, interleaved,
                want_v, q, k, v)
 
 
 def minf_kv_write(k, v, cache: KVCache, pages, start, count=None, rows=None, ws=None, stream=None):
     """Writes k, v [B, Hkv, M, d] (d contiguous, other strides multiples of 8) into the cache at positions
     start[b] + i, i < count[b] (see include/minf.h); with `rows` [B, N] position start[b] + i gets row rows[b, i]."""
-    _on(stream, _binding().kv_write, k, v, cache._addr, cache.k, pages, start, count, rows, ws)
+    _on(stream, cache.device, _binding().kv_write, k, v, cache._addr, cache.k, pages, start, count, rows, ws)
 
 
 def minf_kv_read(cache: KVCache, pages, lens, N, k=None, v=None, ws=None, stream=None):
     """Positions 0 .. N-1 of every sequence as dense bf16 k, v [B, Hkv, N, d], zeros from lens[b] on."""
-    return _on(stream, _binding().kv_read, cache._addr, cache.k, pages, lens, N, k, v, ws)
+    return _on(stream, cache.device, _binding().kv_read, cache._addr, cache.k, pages, lens, N, k, v, ws)
 
 
 def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=None, o=None, lse=None, want_lse=True,
@@ -555,5 +556,5 @@ def minf_tree_attn(q, cache: KVCache, pages, ctx_lens, n_draft=None, tree_mask=N
     ctx_lens[b] context positions (see include/minf.h).  tree_mask [B, T] int64: bit u of word t lets token t see
     token u; None is a chain.  n_draft [B] int32: tokens of each sequence (None: T); rows behind them are not
     written (a new `o` is not initialised there).  lse is None without `want_lse`."""
-    return _on(stream, _binding().tree_attn, q, cache._addr, cache.k, pages, ctx_lens, n_draft, tree_mask, o, lse,
+    return _on(stream, cache.device, _binding().tree_attn, q, cache._addr, cache.k, pages, ctx_lens, n_draft, tree_mask, o, lse,
                want_lse, scale, ws)

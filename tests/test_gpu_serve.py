@@ -676,3 +676,15 @@ def test_calls_on_two_streams_at_once():
         assert minf.minf_get_device_status(ws[s]) == 0
         for o, lse in outs[s]:
             assert torch.equal(o, a["o"]) and torch.equal(lse, a["lse"])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_row_groups(e4m3):
+    """One KV head for all queries: 2048 rows in 16 groups, some of a shorter sequence's groups without rows."""
+    run_tree(51, 2, 32, 1, 64, 64, [500, 3], [64, 9], 64, e4m3, "tree")
+    run_tree(52, 1, 12, 1, 128, 64, [300], [33], 16, e4m3, "chain")
+
+
+def test_head_counts_and_single_rows():
+    for Hq, Hkv, T in ((5, 5, 1), (10, 2, 3), (16, 1, 1), (17, 1, 1), (33, 1, 2), (64, 1, 1), (65, 1, 1), (128, 1, 1)):
+        run_tree(Hq, 1, Hq, Hkv, 64, T, [190], [T], 32, Hq % 2 == 0, "chain")
