@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
-  } else if (warp == 0) {
+  }
+  wait_prerequisite();  // nothing of global memory is read before this
+  if (warp == 0) {
     const Walk w = block_share(p, part_lane);
     if (lane == 0) *start = w;
   }
@@ -737,6 +739,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   const int bh = blockIdx.y, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
   const int rg = blockIdx.x / nr, r = blockIdx.x % nr;  // nr rows of each row group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
   int ctx;
   const int nd = new_tokens(p, b, ctx), nt = tiles(ctx, nd);
   int c0 = 0;
@@ -806,8 +809,7 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Tree
   using C = Cfg<D, F8, NR>;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  tree_attn_kernel<D, F8, NR><<<p.lanes * p.groups, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
-  return cudaGetLastError();
+  return launch_early(tree_attn_kernel<D, F8, NR>, dim3(p.lanes * p.groups), C::kThreads, C::kSmem, stream, tk, tv, p);
 }
 
 template <int D, bool F8>
@@ -824,16 +826,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams p, c
                                  : tree_wide_launch(D, tk, tv, p, stream);
   if (e != cudaSuccess) return e;
   const int nr = (int)std::min<long long>(p.rows, rows);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.groups * nr), (unsigned)bh);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p, nr);
+  return launch_early(tree_join_kernel<D>, dim3((unsigned)(p.groups * nr), (unsigned)bh), 256, 0, stream, p, nr);
 }
 
 }  // namespace

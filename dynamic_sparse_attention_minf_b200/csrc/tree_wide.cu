@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
-  } else if (warp == 0) {
+  }
+  if (warp == 0) {
     const Walk w = block_share(p, part_lane);
     if (lane == 0) *start = w;
   }
@@ -514,6 +515,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParam
   using C = Wide<D, F8>;
   cudaError_t e = cudaFuncSetAttribute(tree_wide_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
+  // not ahead of its predecessor's end, as tree_attn.cu's are: long calls in a row
+  // took 172 us instead of 168
   tree_wide_kernel<D, F8><<<p.lanes * p.groups, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }

@@ -688,3 +688,66 @@ def test_many_row_groups(e4m3):
 def test_head_counts_and_single_rows():
     for Hq, Hkv, T in ((5, 5, 1), (10, 2, 3), (16, 1, 1), (17, 1, 1), (33, 1, 2), (64, 1, 1), (65, 1, 1), (128, 1, 1)):
         run_tree(Hq, 1, Hq, Hkv, 64, T, [190], [T], 32, Hq % 2 == 0, "chain")
+
+
+@pytest.mark.parametrize("T,e4m3", [(1, True), (40, False)])
+def test_attention_follows_what_comes_before_it(T, e4m3):
+    """The attention may begin before its predecessor in the stream is over, and must not read early: behind a
+    kernel, a copy and a fill that change its inputs, in a row and captured into a graph."""
+    a = run_tree(61, 1, 8, 2, 128, T, [2100], [T], 64, e4m3, "chain")
+    b = run_tree(62, 1, 8, 2, 128, T, [900], [T], 64, e4m3, "chain")
+    n = max(a["pages"].shape[1], b["pages"].shape[1])
+    wide = lambda r: torch.cat([r["pages"], r["pages"][:, :1].expand(1, n - r["pages"].shape[1])], 1).contiguous()  # noqa: E731
+    q, ctx, pages = a["q"].clone(), a["ctx"].clone(), wide(a)
+    o, lse = torch.empty_like(a["o"]), torch.empty_like(a["lse"])
+    pa, pb = wide(a), wide(b)
+    big = torch.empty(64 << 20, device="cuda")
+    flat = minf.KVCache.empty(a["c"].n_pages + b["c"].n_pages, 2, 64, 128, e4m3)   # both caches' pages in one pool
+    for name in ("k", "v") + (("k_exp", "v_exp") if e4m3 else ()):
+        t = getattr(flat, name)
+        both = torch.cat([getattr(r["c"], name).view(torch.uint8).flatten() for r in (a, b)])
+        t.view(torch.uint8).copy_(both.view(t.view(torch.uint8).shape))
+    pb = pb + a["c"].n_pages
+    ws = a["ws"]
+
+    def step(r, p, slow):
+        if slow:
+            big.normal_()                                        # a long kernel before the changes
+        q.copy_(r["q"])
+        pages.copy_(p)
+        ctx.fill_(0)
+        ctx.add_(int(r["ctx"][0]) if not torch.cuda.is_current_stream_capturing() else r["len"])
+        minf.minf_tree_attn(q, flat, pages, ctx, o=o, lse=lse, ws=ws)
+
+    a["len"], b["len"] = 2100, 900
+    for i in range(6):
+        r, p = ((a, pa), (b, pb))[i % 2]
+        step(r, p, i % 3 == 0)
+        assert torch.equal(o, r["o"]) and torch.equal(lse, r["lse"])
+    # calls in a row, each over the other's lengths, without a look between them
+    got = []
+    for i in range(8):
+        r, p = ((a, pa), (b, pb))[i % 2]
+        ctx.copy_(r["ctx"])
+        pages.copy_(p)
+        got.append(minf.minf_tree_attn(r["q"], flat, pages, ctx, ws=ws))
+    for i, (oi, li) in enumerate(got):
+        r = (a, b)[i % 2]
+        assert torch.equal(oi, r["o"]) and torch.equal(li, r["lse"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(graph):
+        for r, p in ((a, pa), (b, pb), (a, pa)):
+            step(r, p, False)
+            outs.append((o.clone(), lse.clone()))
+        lse.zero_()
+        minf.minf_tree_attn(q, flat, pages, ctx, o=o, lse=lse, ws=ws)
+    for _ in range(3):
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for r, (oi, li) in zip((a, b, a), outs):
+            assert torch.equal(oi, r["o"]) and torch.equal(li, r["lse"])
+        assert torch.equal(o, a["o"]) and torch.equal(lse, a["lse"])
+    assert minf.minf_get_device_status(ws) == 0
