@@ -12,7 +12,7 @@
 
 #include <type_traits>
 
-#include "minf_device.cuh"
+#include "serve_device.cuh"
 #include "serve_internal.h"
 
 namespace minf {
@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
   const int bh = blockIdx.x / chunks, h = bh % p.c.Hkv, b = bh / p.c.Hkv;
   const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
+  launch_dependents();
+  wait_prerequisite();
   int count = p.count ? __ldg(p.count + b) : p.N;
   if (count < 0 || count > p.N) {
     if (threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 100);
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p,
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
   const int bh = blockIdx.x / chunks, h = bh % p.c.Hkv, b = bh / p.c.Hkv;
   const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
+  launch_dependents();
+  wait_prerequisite();
   using Raw = typename std::conditional<F8, uint2, uint4>::type;
   const int len = min(__ldg(p.lens + b), p.N);
   // lane u of a group finds its row u, and reads that row's exponents
@@ -214,14 +218,12 @@ int chunks_of(int N) {
 template <int D, bool F8>
 cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
   const int chunks = chunks_of<D>(p.N);
-  kv_write_kernel<D, F8><<<(unsigned)(p.B * p.c.Hkv * chunks), kThreads, 0, stream>>>(p, chunks);
-  return cudaGetLastError();
+  return launch_early(kv_write_kernel<D, F8>, dim3((unsigned)(p.B * p.c.Hkv * chunks)), kThreads, 0, stream, p, chunks);
 }
 template <int D, bool F8>
 cudaError_t launch_read(const KvReadParams& p, cudaStream_t stream) {
   const int chunks = chunks_of<D>(p.N);
-  kv_read_kernel<D, F8><<<(unsigned)(p.B * p.c.Hkv * chunks), kThreads, 0, stream>>>(p, chunks);
-  return cudaGetLastError();
+  return launch_early(kv_read_kernel<D, F8>, dim3((unsigned)(p.B * p.c.Hkv * chunks)), kThreads, 0, stream, p, chunks);
 }
 
 }  // namespace

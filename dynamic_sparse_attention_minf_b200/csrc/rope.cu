@@ -11,7 +11,7 @@
 // else is in 32 bits with one rounding at the end.
 #include <algorithm>
 
-#include "minf_device.cuh"
+#include "serve_device.cuh"
 #include "serve_internal.h"
 
 namespace minf {
@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, i
   __shared__ float2 angles[8][kThreads];  // (cos, sin) of each thread's elements, read by it alone
   const int lane = threadIdx.x % L;
   const long long item = (long long)blockIdx.x * kRows + threadIdx.x / L;
+  launch_dependents();
+  wait_prerequisite();
   if (item >= (long long)p.B * p.N * chunks) return;
   const unsigned group = (L == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) - lane);  // the group's lanes of the warp
   const int tok = (int)(item / chunks), h0 = (int)(item % chunks) * hb;
@@ -151,8 +153,8 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   const int hb = (int)std::min<long long>(heads, std::max<long long>(1, tokens * heads / 16384));
   const int chunks = (heads + hb - 1) / hb;
   const int rows = kThreads / (D / 8);
-  rope_kernel<D><<<(unsigned)((tokens * chunks + rows - 1) / rows), kThreads, 0, stream>>>(p, hb, chunks);
-  return cudaGetLastError();
+  return launch_early(rope_kernel<D>, dim3((unsigned)((tokens * chunks + rows - 1) / rows)), kThreads, 0, stream, p, hb,
+                      chunks);
 }
 
 }  // namespace

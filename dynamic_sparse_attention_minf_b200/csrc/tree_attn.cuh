@@ -27,26 +27,6 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (unsigned)(a + b - 1) / (unsigned)b; }
 
-// Launches a kernel that may begin before the one before it in the stream is over,
-// and waits for that (wait_prerequisite) before it touches global memory.  A
-// kernel lets the next begin (launch_dependents) when all of its own blocks are
-// resident, so none that waits can keep out one that is waited for.
-template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                         Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
-}
-
 // How the work is cut, for a whole warp: in runs of `per` tiles of the list
 // (sequence-major, then KV head, then tile), or, with at most one sequence and
 // head per block, each of these into pieces of at most `per` tiles.  `units` of
