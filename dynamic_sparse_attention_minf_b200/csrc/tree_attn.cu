@@ -101,6 +101,8 @@ struct Cfg {
   // use the top of their range; a score kTop above the reference moves it
   static constexpr float kOff = F8 ? 4.f : 0.f, kTop = F8 ? 15.f : 16.f;
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
+  // a softmax warpgroup that reads exponents is less than a round of the ring ahead
+  static_assert(!F8 || kKStages >= kWG, "rounds that a wait can tell apart");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(24 * NR <= kPB && 4 * kWG * NR <= kQB, "scratch in the idle P and Q buffers");
   static_assert(NR * D * 2 <= kWG * kPB && kWG * (kSCols + kOCols) <= kTmem, "the queries as they are in the idle P buffers");
@@ -623,7 +625,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
           if (decltype(masked)::value && !in) {
             // what lies behind the sequence's end may be anything: zero weight
             // needs a finite value
-            const int st = it % C::kVStages;
+            const int st = it % C::kVStages, was = it - C::kVStages;
+            // A wait tells only odd rounds of the ring from even ones.  With fewer
+            // stages than warpgroups the stage's former tile may not even have landed:
+            // its product, which this one's load waits for as well, comes first.
+            if (C::kVStages < C::kWG && was >= 0)
+              mbar_wait_or_abort(&pv_done[was % C::kWG], (was / C::kWG) & 1, abort, p.status, 126);
             mbar_wait_or_abort(&v_full[st], (it / C::kVStages) & 1, abort, p.status, 126);
             uint8_t* v = smem + C::kOffV + st * C::kTileB + tid * C::kPitch;
 #pragma unroll

@@ -751,3 +751,22 @@ def test_attention_follows_what_comes_before_it(T, e4m3):
             assert torch.equal(oi, r["o"]) and torch.equal(li, r["lse"])
         assert torch.equal(o, a["o"]) and torch.equal(lse, a["lse"])
     assert minf.minf_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,Hkv,T,longest,d", [(20, 8, 5, 4241, 128), (24, 8, 8, 2600, 128), (32, 8, 1, 939, 128),
+                                               (16, 8, 16, 700, 128), (20, 4, 5, 4241, 64), (6, 4, 40, 1500, 128)])
+def test_value_tiles_that_come_late(B, Hkv, T, longest, d, e4m3):
+    """Batches of many last tiles (part keys, part rows to be cleared) whose values are still on their way, some of
+    them from memory, when their scores are done: right, and the same bits every time."""
+    rng = np.random.default_rng(longest)
+    ctx = np.full(B, longest)
+    ctx[::3] = rng.integers(1, longest, len(ctx[::3]))
+    r = run_tree(71, B, 4 * Hkv, Hkv, d, T, ctx, np.full(B, T), 64, e4m3, "tree")
+    fill = torch.empty(64 << 20, device="cuda")
+    for i in range(24):
+        if i % 2:
+            fill.zero_()                                         # 256 MB: the cache is read from memory again
+        o, lse = minf.minf_tree_attn(r["q"], r["c"], r["pages"], r["ctx"], tree_mask=r["tm"], ws=r["ws"])
+        assert torch.equal(o, r["o"]) and torch.equal(lse, r["lse"]), i
+    assert minf.minf_get_device_status(r["ws"]) == 0
