@@ -132,6 +132,9 @@ __device__ __forceinline__ float lane_totals(float (&v)[N]) {
   return v[0];
 }
 
+// What a sum was before x joined it; nothing when the two overflowed.
+__device__ __forceinline__ float without(float sum, float x) { return sum == INFINITY ? 0.f : sum - x; }
+
 template <int D, bool F8, int NR>
 __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -542,7 +545,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                 }
                 tmem_wait_st();
                 // l without the weights that the first pass added: they are formed
-                // again.  Below 2^-90 what was there before them does not count.
+                // again.  Both are still sums of 2^s in the former reference, so the
+                // difference is off by a rounding of what is formed again at most.
+                // Where they overflow, the weight is above 2^127, and what was there
+                // before it, weights up to 2^15 times 2^80 each, does not count.
 #pragma unroll
                 for (int c0 = 0; c0 < NR; c0 += 16) {
                   uint32_t s[16], lo[16];
@@ -554,8 +560,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                     float t0, t1, l0, l1;
                     exponent2(masked, s[c], s[c + 1], r, nwas, t0, t1);
                     f32x2_unpack(l[r / 2], l0, l1);
-                    l0 = shrink[r] < 0x1p-90f ? 0.f : (l0 - fast_exp2(t0) * inv) * shrink[r];
-                    l1 = shrink[r + 1] < 0x1p-90f ? 0.f : (l1 - fast_exp2(t1) * inv) * shrink[r + 1];
+                    l0 = without(l0, fast_exp2(t0) * inv) * shrink[r];
+                    l1 = without(l1, fast_exp2(t1) * inv) * shrink[r + 1];
                     l[r / 2] = f32x2_pack(l0, l1);
                   }
                 }

@@ -1,0 +1,100 @@
+"""Attention over the cache where keys weigh very differently and so do their
+values: rows of one channel, of zeros and of tiny numbers, beside a long context
+whose tiles all fall to one block (its running reference and sums see every one
+of them).
+
+Tolerances are those of test_gpu_serve.py (u = 2^-8; a score is off by e_s), and
+2^-17 for the log-sum-exp: with values' powers of two down to 2^-80 its three
+32-bit sums of numbers up to 128 round by 2^-18 each, in powers of two.
+"""
+import math
+
+import pytest
+import torch
+
+from dynamic_sparse_attention_minf_b200 import minf
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    minf.lib()
+
+
+def exact(q, k, v, ctx, scale):
+    """Float64 form of a chain: q [Hq, T, d] over one KV head's k, v [ctx + T, d]: O, LSE, sum p|v|, p."""
+    T = q.shape[1]
+    j = torch.arange(ctx + T, device=q.device)
+    s = (q.double() @ k.double().T * scale).masked_fill(j[None] > ctx + torch.arange(T, device=q.device)[:, None], -math.inf)
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[..., None])
+    return p @ v.double(), lse, p @ v.double().abs(), p
+
+
+def one_block(rows, d, e4m3, nats, where, edit, seed=0, L=8192, B=150):
+    """B sequences that share one cached sequence of L context keys, of scores within a nat or two of each other
+    except for the key at `where`, `nats` above; edit(v, where) makes the values.  More sequences than blocks, so
+    that a block takes the tiles of a whole sequence in a row.  Returns what check() looks at."""
+    G = 4
+    T = rows // G
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    scale = d ** -0.5
+    k, v, q = (torch.randn(1, h, n, d, generator=g, device="cuda") for h, n in ((1, L + T), (1, L + T), (G, T)))
+    k *= 0.5
+    q[..., 0], k[..., 0] = 16.0, 0.0
+    k[0, 0, where] = 0
+    k[0, 0, where, 0] = nats / (16 * scale)
+    v = 1 + 0.3 * v
+    edit(v[0, 0], where)
+    q, k, v = (t.to(torch.bfloat16) for t in (q, k, v))
+    n = -(-(L + T) // 64)
+    c = minf.KVCache.empty(n, 1, 64, d, e4m3)
+    pages = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    ws = minf.tree_attn_workspace(B, G, 1, T, d)
+    minf.minf_kv_write(k, v, c, pages, torch.zeros(1, **I32), ws=ws)
+    kd, vd = minf.minf_kv_read(c, pages, torch.full((1,), L + T, **I32), L + T, ws=ws)
+    o, lse = minf.minf_tree_attn(q.expand(B, -1, -1, -1).contiguous(), c, pages.expand(B, -1).contiguous(),
+                                 torch.full((B,), L, **I32), ws=ws)
+    assert minf.minf_get_device_status(ws) == 0
+    exps = c.v_exp[pages[0].long()].flatten()[:L + T].double() - 127 if e4m3 else None
+    return q[0], kd[0, 0], vd[0, 0], L, scale, o, lse, exps
+
+
+def check(q, k, v, ctx, scale, o, lse, exps, floor=0.0):
+    """`floor`: 8-bit weights, times their values' powers of two, may be off by this part of the row's largest."""
+    O, L, A, p = exact(q, k, v, ctx, scale)
+    k64, q64 = k.double(), q.double()
+    es = scale * (2.0 ** -17 * q64.norm(dim=-1) * k64.norm(dim=-1).max()
+                  + (2.0 ** -18 * q64.abs().amax(-1) * k64.abs().sum(-1).max() if exps is not None else 0.0))
+    tol = U * O.abs() + (U + 2 * es[..., None]) * A + 2.0 ** -120
+    if floor:
+        live = (v != 0).any(-1)
+        top = (p * torch.exp2(exps) * live).amax(-1, keepdim=True)
+        tol = tol + floor * top * (v.double().abs() * torch.exp2(-exps)[:, None]).sum(0)
+    err = (o.double() - O).abs()
+    assert (err <= tol).all(), ((err / tol).max().item(), err.max().item())
+    err = (lse.double() - L).abs()
+    assert (err <= es + 2.0 ** -20 * (1 + L.abs()) + 2.0 ** -17).all(), err.max().item()
+
+
+ROWS = [4, 32, 64, 256]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("nats", [8, 40])
+def test_sums_of_tiny_values_outlive_a_move(rows, nats, e4m3):
+    """A context of values near 1e-24, then, in a later tile, a key 8 nats above it with values near 200: the sums
+    before it are most of the total, although weight times value moves by 2^90.  And one 40 nats above it with tiny
+    values too: its weight overflows against the reference of the tiles before it."""
+    def tiny(v, where):
+        v *= 1e-24
+        if nats == 8:
+            v[where] *= 2e26
+    check(*one_block(rows, 128, e4m3, nats, 6000, tiny))
