@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                     l0 = without(l0, fast_exp2(t0) * inv) * shrink[r];
                     l1 = without(l1, fast_exp2(t1) * inv) * shrink[r + 1];
                     l[r / 2] = f32x2_pack(l0, l1);
+                    asm volatile("" ::: "memory");  // one pair's factors at a time (8-bit, 64 rows: 384 bytes spilled without)
                   }
                 }
               }
