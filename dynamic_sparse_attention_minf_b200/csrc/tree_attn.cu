@@ -408,11 +408,23 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         const int j0 = (w.t0 + i) * 128, j = j0 + tid, u = j - w.ctx;
         const bool in = j < len;
         const int kst = it % C::kKStages;
+        // the thread's row of the tile's values, once they have landed
+        auto value_row = [&] {
+          // A wait tells only odd rounds of the ring from even ones, so the stage's
+          // former tile has to be known to have landed: by its product when there are
+          // fewer stages than warpgroups (this tile's load waits for that as well), by
+          // that of this warpgroup's tile before, which is no earlier, otherwise.
+          const int st = it % C::kVStages, was = it - (C::kVStages < C::kWG ? C::kVStages : C::kWG);
+          if (was >= 0) mbar_wait_or_abort(&pv_done[was % C::kWG], (was / C::kWG) & 1, abort, p.status, 126);
+          mbar_wait_or_abort(&v_full[st], (it / C::kVStages) & 1, abort, p.status, 126);
+          return smem + C::kOffV + st * C::kTileB + tid * C::kPitch;
+        };
         float km = 0.f, lv = 0.f, inv = 1.f;  // 2^key exponent, value exponent, its inverse power
+        bool zeros = false;  // whether a row of the warp's keys may be of zeros
         if constexpr (F8) {
           mbar_wait_or_abort(&k_full[kst], (it / C::kKStages) & 1, abort, p.status, 122);
           const uint8_t* e = smem + C::kOffExp + kst * C::kExpB + tid;
-          const uint32_t ke = e[0], ve = e[128];
+          const uint32_t ke = e[0], ve = max((uint32_t)e[128], kLeastExp);
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_empty[kst]);
           if (in) {
@@ -420,9 +432,19 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
             lv = ve == 255u ? NAN : (float)((int)ve - 127);
             inv = ve == 255u ? NAN : __uint_as_float((254u - ve) << 23);
           }
+          zeros = __any_sync(0xFFFFFFFFu, in && ve == kZeroExp);
         }
         mbar_wait_or_abort(&s_full[wg], uses & 1, abort, p.status, 123);
         tc_fence_after();
+        if (zeros) {
+          // A row of zeros adds nothing to O, so it must not raise the reference, as
+          // the power 2^0 that it is stored with would
+          if (in && lv == (float)((int)kZeroExp - 127) && zero_row<C::kPitch>(value_row())) {
+            lv = (float)((int)kLeastExp - 127);
+            inv = __uint_as_float((254u - kLeastExp) << 23);
+          }
+          __syncwarp();
+        }
         // scores of rows c0 .. of the thread's key: asked for, and taken
         auto ask = [&](int c0, auto& s, auto& lo) {
           tmem_ld(s_col + c0, s);
@@ -632,14 +654,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
           if (decltype(masked)::value && !in) {
             // what lies behind the sequence's end may be anything: zero weight
             // needs a finite value
-            const int st = it % C::kVStages, was = it - C::kVStages;
-            // A wait tells only odd rounds of the ring from even ones.  With fewer
-            // stages than warpgroups the stage's former tile may not even have landed:
-            // its product, which this one's load waits for as well, comes first.
-            if (C::kVStages < C::kWG && was >= 0)
-              mbar_wait_or_abort(&pv_done[was % C::kWG], (was / C::kWG) & 1, abort, p.status, 126);
-            mbar_wait_or_abort(&v_full[st], (it / C::kVStages) & 1, abort, p.status, 126);
-            uint8_t* v = smem + C::kOffV + st * C::kTileB + tid * C::kPitch;
+            uint8_t* v = value_row();
 #pragma unroll
             for (int x = 0; x < C::kRegions; ++x)
 #pragma unroll

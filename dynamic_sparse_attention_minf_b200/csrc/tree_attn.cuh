@@ -10,6 +10,21 @@ namespace minf {
 
 constexpr int kMaxBlocks = 148;  // one block per SM
 constexpr float kFloor = -1e30f; // reference of a row that has seen nothing
+// Stored exponents of 8-bit values: of a row of zeros (and of rows with their
+// largest in (224, 448]), and the least one.
+constexpr uint32_t kZeroExp = 127, kLeastExp = 127 - 80;
+
+// Whether the 8-bit values of a row in shared memory are all zeros.
+template <int Bytes>
+__device__ __forceinline__ bool zero_row(const uint8_t* row) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int o = 0; o < Bytes; o += 16) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + o);
+    any |= x.x | x.y | x.z | x.w;
+  }
+  return (any & 0x7f7f7f7fu) == 0;
+}
 
 __device__ __forceinline__ int new_tokens(const TreeParams& p, int b, int& ctx) {
   ctx = __ldg(p.ctx + b);

@@ -294,22 +294,39 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
         // the half's keys: 2^key exponent, value exponent, its inverse power (four keys a read)
         float* key_pow = reinterpret_cast<float*>(smem + C::kOffKey) + b * 384 + wg * 64;
         float *val_exp = key_pow + 128, *val_inv = key_pow + 256;
+        bool ask = false, zeros = false;  // whether this key's (a key's) row may be of zeros
         if constexpr (F8) {
           if (tid < 64) {
             mbar_wait_or_abort(&k_full[kst], (it / C::kKStages) & 1, abort, p.status, 122);
             const uint8_t* e = smem + C::kOffExp + kst * C::kExpB + wg * 64 + tid;
-            const uint32_t ke = e[0], ve = e[128];
+            const uint32_t ke = e[0], ve = max((uint32_t)e[128], kLeastExp);
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_empty[kst]);
             const bool in = j0 + tid < len;
             key_pow[tid] = !in ? 0.f : ke == 255u ? NAN : __uint_as_float(ke << 23);
             val_exp[tid] = !in ? 0.f : ve == 255u ? NAN : (float)((int)ve - 127);
             val_inv[tid] = !in ? 1.f : ve == 255u ? NAN : __uint_as_float((254u - ve) << 23);
+            ask = in && ve == kZeroExp;
           }
-          named_bar_sync(bar_wg, 128);
+          zeros = !bar_and(bar_wg, 128, !ask);
         }
         mbar_wait_or_abort(&s_full[b], (it >> 1) & 1, abort, p.status, 123);
         tc_fence_after();
+        if (zeros) {
+          // A row of zeros adds nothing to O, so it must not raise the reference, as the
+          // power 2^0 that it is stored with would.  (This tile's scores were issued
+          // behind the product of the tile before the last, so its values' stage is at
+          // most one round behind and the wait is for the right one.)
+          if (ask) {
+            const int st = it % C::kVStages;
+            mbar_wait_or_abort(&v_full[st], (it / C::kVStages) & 1, abort, p.status, 126);
+            if (zero_row<C::kPitch>(smem + C::kOffV + st * C::kTileB + (wg * 64 + tid) * C::kPitch)) {
+              val_exp[tid] = (float)((int)kLeastExp - 127);
+              val_inv[tid] = __uint_as_float((254u - kLeastExp) << 23);
+            }
+          }
+          named_bar_sync(bar_wg, 128);
+        }
         uint32_t s[2][32];
         tmem_ld(s_col, s[0]);
         tmem_ld(s_col + 32, s[1]);

@@ -98,3 +98,33 @@ def test_sums_of_tiny_values_outlive_a_move(rows, nats, e4m3):
         if nats == 8:
             v[where] *= 2e26
     check(*one_block(rows, 128, e4m3, nats, 6000, tiny))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("nats,where", [(8, 0), (10, 0), (12, 5000), (14, 0), (16, 8190)])
+def test_zero_row_beside_far_scores(rows, nats, where, e4m3):
+    """A key whose values are all zero (a sink, a padding row) far above the others, which still hold a good part
+    of the sum: it adds nothing, and takes nothing from the others' bits."""
+    def zero(v, where):
+        v[where] = 0
+    check(*one_block(rows, 128 if nats != 12 else 64, e4m3, nats, where, zero))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_zero_rows_among_large_ones(rows):
+    """Rows of zeros and rows that share their stored exponent (largest value in (224, 448]), in every tile and in
+    the last, part-filled one; only zeros; and a pool of zeros that was never written."""
+    def mixed(v, where):
+        v *= 250
+        v[::5] = 0
+        v[1::7, 1:] = 0                                          # zero but for one channel
+    check(*one_block(rows, 128, True, 9, 1000, mixed, L=2077))
+    check(*one_block(rows, 64, True, 9, 100, lambda v, where: v.zero_(), L=1000))
+    c = minf.KVCache.empty(3, 1, 64, 128, True)
+    q = torch.randn(1, 4, rows // 4, 128, device="cuda").to(torch.bfloat16)
+    ws = minf.tree_attn_workspace(1, 4, 1, rows // 4, 128)
+    o, lse = minf.minf_tree_attn(q, c, torch.arange(3, **I32)[None], torch.full((1,), 100, **I32), ws=ws)
+    assert minf.minf_get_device_status(ws) == 0 and (o == 0).all()
+    want = torch.log(101.0 + torch.arange(rows // 4, device="cuda"))
+    assert ((lse - want).abs() <= 2.0 ** -16).all()              # 2^-17, and that log's own rounding
