@@ -26,9 +26,10 @@
 //    in the rare tile where it happens.
 //  * 8-bit keys and values enter the 8-bit product as they are.  The query row is
 //    brought to [128, 256) by a power of two and split into two e4m3 parts, which
-//    hold bf16's 8 bits; the weight (times the value's power of two) into three
-//    e5m2 parts, 9 bits, whose range of 2^32 keeps small weights beside a
-//    dominant one.
+//    hold bf16's 8 bits (fewer of elements below 2^-9 of the row's largest); the
+//    weight (times the value's power of two) into three e5m2 parts, 9 bits, down to
+//    2^-29 of the row's largest: each part is kept 2^4 larger than the one before,
+//    or their common lowest step would end that at 2^-21.
 //  * The work is cut evenly over the blocks, one per SM.  Few sequences (at most
 //    one per block, counted with their KV heads) are each cut into pieces, so that
 //    no block pays for two sequences' beginning and end.  Many form one list of
@@ -98,8 +99,10 @@ struct Cfg {
   static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, kOCols, 0, 1, 1, 1) : idesc_bf16(128, NR, 1, 1);
   static constexpr int kCh = NR == 64 ? 32 : 16;              // columns a thread takes at once
   // the weights' references lie kOff below the maximum seen, so that 8-bit parts
-  // use the top of their range; a score kTop above the reference moves it
+  // use the top of their range; a score kTop above the reference moves it (kOff 8
+  // moves it more often: 64 rows over 128K 8-bit positions 114 us, 107 with 4)
   static constexpr float kOff = F8 ? 4.f : 0.f, kTop = F8 ? 15.f : 16.f;
+  static constexpr float kPartScale = F8 ? 0.0625f : 1.f;  // of each 8-bit part beside the one before
   static_assert(kVStages >= 2 && kKStages >= 2, "rings");
   // a softmax warpgroup that reads exponents is less than a round of the ring ahead
   static_assert(!F8 || kKStages >= kWG, "rounds that a wait can tell apart");
@@ -625,14 +628,18 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
                   if constexpr (F8) {
                     // e5m2 is the upper byte of a half: each part is the remainder
                     // rounded there (half a step up, in magnitude), and leaves an
-                    // exact remainder.  A NaN weight may be lost here, not in l.
+                    // exact remainder, of which 16 times is the next part, so that
+                    // the last reaches down to a half's lowest step (no part is
+                    // above 2^15: a remainder is at most an eighth).  A NaN weight
+                    // may be lost here, not in l.
+                    const __half2 up = __float2half2_rn(1.f / C::kPartScale);
 #pragma unroll
                     for (int q = 0; q < 3; ++q) {
                       const uint32_t a = h[0] + 0x00800080u, b = h[1] + 0x00800080u;
                       out[q][c / 4] = __byte_perm(a, b, 0x7531);
                       const uint32_t ta = a & 0xff00ff00u, tb = b & 0xff00ff00u;
-                      const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&h[0]), *reinterpret_cast<const __half2*>(&ta));
-                      const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&h[1]), *reinterpret_cast<const __half2*>(&tb));
+                      const __half2 ra = __hmul2(up, __hsub2(*reinterpret_cast<const __half2*>(&h[0]), *reinterpret_cast<const __half2*>(&ta)));
+                      const __half2 rb = __hmul2(up, __hsub2(*reinterpret_cast<const __half2*>(&h[1]), *reinterpret_cast<const __half2*>(&tb)));
                       h[0] = *reinterpret_cast<const uint32_t*>(&ra);
                       h[1] = *reinterpret_cast<const uint32_t*>(&rb);
                     }
@@ -729,11 +736,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
           if (!has(v)) continue;  // its O^T is not of this segment
 #pragma unroll
           for (int q = 0; q < C::kPStack; ++q) {
+            const float scale = q == 0 ? 1.f : q == 1 ? C::kPartScale : C::kPartScale * C::kPartScale;
             uint32_t o[8];
             tmem_ld(lanes + C::kOffO + v * C::kOCols + q * NR + c0, o);
             tmem_landed(o);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = fmaf(__uint_as_float(o[c]), weight[v * NR + c0 + c], x[c]);
+            for (int c = 0; c < 8; ++c) x[c] = fmaf(__uint_as_float(o[c]) * scale, weight[v * NR + c0 + c], x[c]);
           }
         }
         if (tid < D) {

@@ -54,8 +54,10 @@ struct Wide {
   static constexpr int kOffO = 256;                 // TMEM: S of two tiles (128 columns each), then O of two halves
   static constexpr uint32_t kIdescS = F8 ? idesc_f8(128, 128, 0, 0, 0, 0) : idesc_bf16(128, 128, 0, 0);
   static constexpr uint32_t kIdescO = F8 ? idesc_f8(128, D, 1, 0, 0, 1) : idesc_bf16(128, D, 0, 1);
-  // the weights' reference lies kOff below the maximum seen; kTop above it, it moves
-  static constexpr float kOff = F8 ? 4.f : 0.f, kTop = F8 ? 15.f : 8.f;
+  // the weights' reference lies kOff below the maximum seen; kTop above it, it moves.
+  // The three 8-bit parts share one accumulator and its lowest step, 2^-16: weights
+  // are held to half of that, 2^-27 of the row's largest (kOff 4, 2^-21, is no faster)
+  static constexpr float kOff = F8 ? 10.f : 0.f, kTop = F8 ? 15.f : 8.f;
   static_assert(kVStages >= 2 && kKStages >= 2 && kSmem <= 232448, "shared memory");
 };
 

@@ -496,9 +496,19 @@ size_t minf_tree_attn_workspace(int B, int Hq, int Hkv, int T, int d);
  * n_draft[b] on are ignored.  A row that sees nothing gets O = 0 and lse =
  * -inf; rows t >= n_draft[b] are not written.  scale <= 0 selects 1/sqrt(d).
  * T * Hq / Hkv <= 18,944, B * Hkv <= 65,535, and B * Hkv * max_pages * page <
- * 2^37.  Scores, softmax and sums in 32 bits.  Cache rows outside what a sequence
- * holds may contain anything.  The values of drafted tokens that a token does
- * not see must be finite (their weight is zero, not skipped).
+ * 2^37.  Cache rows outside what a sequence holds may contain anything.  The
+ * values of drafted tokens that a token does not see must be finite (their weight
+ * is zero, not skipped).  A row all of whose scores are -infinity counts as one
+ * that sees nothing.
+ *
+ * Scores, softmax and sums are held in 32 bits, with these roundings.  16-bit
+ * cache: the weights are rounded to bf16 before their product with the values.
+ * 8-bit cache: a query's elements keep their 8 bits down to 2^-9 of the row's
+ * largest, and are off by up to 2^-17 of it below that.  The weights, times
+ * their value row's power of two, keep 9 bits down to 2^-18 of the row's largest
+ * such product, and are off by up to 2^-27 of it below that; value rows of zeros
+ * do not count in it.  (So a key far above the others hides them in no channel
+ * where they weigh more than that, even where its own values are zero.)
  */
 minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B, int Hq, int T, float scale,
                            const int32_t* pages, int max_pages, const int32_t* ctx_lens, const int32_t* n_draft,

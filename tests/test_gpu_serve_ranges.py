@@ -128,3 +128,17 @@ def test_zero_rows_among_large_ones(rows):
     assert minf.minf_get_device_status(ws) == 0 and (o == 0).all()
     want = torch.log(101.0 + torch.arange(rows // 4, device="cuda"))
     assert ((lse - want).abs() <= 2.0 ** -16).all()              # 2^-17, and that log's own rounding
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("nats,where,size", [(8, 0, 3.0), (10, 5000, 3.0), (12, 0, 3.0), (12, 300, 300.0), (14, 0, 3.0),
+                                             (16, 8190, 3.0), (16, 0, 300.0)])
+def test_one_channel_row_beside_far_scores(rows, nats, where, size, e4m3):
+    """A key far above the others whose values are zero but for one channel: the other channels are what the other
+    keys give, with the bits that the header promises."""
+    def channel(v, where):
+        v[where] = 0
+        v[where, 5] = size
+    floor = (2.0 ** -29 if rows <= 64 else 2.0 ** -27) if e4m3 else 0.0
+    check(*one_block(rows, 128 if nats != 14 else 64, e4m3, nats, where, channel), floor=floor)
