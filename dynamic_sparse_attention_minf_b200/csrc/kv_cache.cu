@@ -30,7 +30,7 @@ __device__ __forceinline__ long long pool_row(const KvView& c, int b, int h, lon
     report(st, MINF_ERR_DEVICE_BOUNDS, where);
     return -1;
   }
-  const int id = __ldg(c.pages + (long long)b * c.max_pages + pi);
+  const int id = load(c.pages + (long long)b * c.max_pages + pi);
   if (id < 0 || id >= c.n_pages) {
     report(st, MINF_ERR_DEVICE_BOUNDS, where + 1);
     return -1;
@@ -96,12 +96,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
   const int n0 = (blockIdx.x % chunks) * (kRows * kUnroll) + grp;
   launch_dependents();
   wait_prerequisite();
-  int count = p.count ? __ldg(p.count + b) : p.N;
+  int count = p.count ? load(p.count + b) : p.N;
   if (count < 0 || count > p.N) {
     if (threadIdx.x == 0) report(p.status, MINF_ERR_DEVICE_BOUNDS, 100);
     count = 0;
   }
-  const int start = __ldg(p.start + b);
+  const int start = load(p.start + b);
   const __nv_bfloat16* kb = p.k + b * p.ksb + h * p.ksh + lane * 8;
   const __nv_bfloat16* vb = p.v + b * p.vsb + h * p.vsh + lane * 8;
   // lane u of a group finds out where its row u comes from and goes to
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
   if (lane < kUnroll) {
     const int n = n0 + lane * kRows;
     if (n < count) {
-      my_src = p.rows ? __ldg(p.rows + (long long)b * p.N + n) : n;
+      my_src = p.rows ? load(p.rows + (long long)b * p.N + n) : n;
       if (my_src < 0 || my_src >= p.M) {
         report(p.status, MINF_ERR_DEVICE_BOUNDS, 101);
         my_src = -1;
@@ -162,13 +162,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p,
   launch_dependents();
   wait_prerequisite();
   using Raw = typename std::conditional<F8, uint2, uint4>::type;
-  const int len = min(__ldg(p.lens + b), p.N);
+  const int len = min(load(p.lens + b), p.N);
   // lane u of a group finds its row u, and reads that row's exponents
   long long my_row = -1;
   uint32_t my_exp = 127 | 127 << 8;
   if (lane < kUnroll && n0 + lane * kRows < len) {
     my_row = pool_row(p.c, b, h, n0 + lane * kRows, p.status, 104);
-    if (F8 && my_row >= 0) my_exp = __ldg(p.c.ke + my_row) | (uint32_t)__ldg(p.c.ve + my_row) << 8;
+    if (F8 && my_row >= 0) my_exp = load(p.c.ke + my_row) | (uint32_t)load(p.c.ve + my_row) << 8;
   }
   Raw rk[kUnroll], rv[kUnroll];
   uint32_t ek[kUnroll], ev[kUnroll];
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p,
     rk[u] = rv[u] = Raw{};
     if (row >= 0) {
       constexpr int kEl = F8 ? 1 : 2;
-      rk[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
-      rv[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
+      rk[u] = load(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.k) + row * D * kEl) + lane);
+      rv[u] = load(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.c.v) + row * D * kEl) + lane);
     }
   }
   if constexpr (F8) {

@@ -59,13 +59,13 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, i
   const bool turn = lane * 8 < p.rot, low = lane < hl;
   const int from = !turn || p.interleaved ? lane : low ? lane + hl : lane - hl;  // of the group
   if (h0 < turned) {
-    const double pos = (double)(p.pos ? __ldg(p.pos + tok) : n) * 0.15915494309189533577;  // 1 / (2 pi)
+    const double pos = (double)(p.pos ? load(p.pos + tok) : n) * 0.15915494309189533577;  // 1 / (2 pi)
     const int i0 = p.interleaved ? lane * 4 : (low ? lane : lane - hl) * 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float sn = 0.f, cs = 1.f;
       if (turn && !(p.interleaved && (e & 1))) {
-        const double turns = pos * __ldg(p.inv_freq + i0 + (p.interleaved ? e / 2 : e));
+        const double turns = pos * load(p.inv_freq + i0 + (p.interleaved ? e / 2 : e));
         sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
         if (p.interleaved || low) sn = -sn;
       } else if (turn) {
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, i
     if (kind < 2) {
       uint4 wr = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wo = wr;  // ones
       if (w) {
-        wr = __ldg(reinterpret_cast<const uint4*>(w) + lane);
-        wo = __ldg(reinterpret_cast<const uint4*>(w) + from);
+        wr = load(reinterpret_cast<const uint4*>(w) + lane);
+        wo = load(reinterpret_cast<const uint4*>(w) + from);
       }
       const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&wr);
       const uint32_t* o2 = reinterpret_cast<const uint32_t*>(&wo);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p, i
       uint4 raw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (h + u < hz) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(h + u) * D));
+        if (h + u < hz) raw[u] = load(reinterpret_cast<const uint4*>(src + (long long)(h + u) * D));
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (h + u >= hz) break;

@@ -141,6 +141,14 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_prerequisite() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// An ordinary load, for whatever an earlier launch may have written.  The read-only
+// path (ld.global.nc) is for memory that nobody writes during the kernel's life, and
+// a kernel that is launched early lives while its predecessor still writes; what the
+// wait makes visible is promised to ordinary loads.
+template <class T>
+__device__ __forceinline__ T load(const T* p) {
+  return *p;
+}
 
 // Launches a kernel that may begin before the one before it in the stream is over,
 // and waits for that (wait_prerequisite) before it touches global memory.  A

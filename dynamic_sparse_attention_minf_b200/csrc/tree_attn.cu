@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, NR>::kThreads, 1)
         for (int i = 0; i < kPieces; ++i) {
           const int c = c0 + i * kStep;
           x[i] = make_uint4(0, 0, 0, 0);
-          if (c < D / 8 && r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (qb + at) * D) + c);
+          if (c < D / 8 && r < rows) x[i] = load(reinterpret_cast<const uint4*>(p.q + (qb + at) * D) + c);
         }
         if (c0 == 0) {
           unsigned long long m = 0;

@@ -27,8 +27,8 @@ __device__ __forceinline__ bool zero_row(const uint8_t* row) {
 }
 
 __device__ __forceinline__ int new_tokens(const TreeParams& p, int b, int& ctx) {
-  ctx = __ldg(p.ctx + b);
-  const int nd = p.ndraft ? __ldg(p.ndraft + b) : p.T;
+  ctx = load(p.ctx + b);
+  const int nd = p.ndraft ? load(p.ndraft + b) : p.T;
   const bool ok = ctx >= 0 && nd >= 0 && nd <= p.T && (long long)ctx + nd <= ((long long)p.c.max_pages << p.c.log_page);
   return ok ? nd : -1;
 }
@@ -174,7 +174,7 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const CUtensorMa
     const int log = p.c.log_page, per_tile = 128 >> log, per_batch = 32 / per_tile;
     const int first = w.t0 * per_tile, end = min(w.t1 * per_tile, (len + (1 << log) - 1) >> log);  // pages
     const int32_t* table = p.c.pages + (long long)w.b * p.c.max_pages;
-    auto fetch = [&](int pg) { return pg + lane < end ? __ldg(table + pg + lane) : 0; };
+    auto fetch = [&](int pg) { return pg + lane < end ? load(table + pg + lane) : 0; };
     int row = 0, ids = fetch(first);  // first pool row of this lane's page of the batch; the next batch
     for (int t = w.t0; t < w.t1; ++t, ++n) {
       const int at = (t - w.t0) % per_batch * per_tile, pages = min(per_tile, end - t * per_tile);

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
         uint4 x[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-          x[i] = tid < rows ? __ldg(reinterpret_cast<const uint4*>(p.q + row * D) + 2 * i + wg) : make_uint4(0, 0, 0, 0);
+          x[i] = tid < rows ? load(reinterpret_cast<const uint4*>(p.q + row * D) + 2 * i + wg) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
           *reinterpret_cast<uint4*>(smem + C::kOffQ + (2 * i + wg) * NR * 16 + tid * 16) = x[i];
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(Wide<D, F8>::kThreads, 1)
             const long long at = qb + (rg * NR + r - tr * p.group) * p.T + tr;
 #pragma unroll
             for (int e = 0; e < E / 2; ++e)
-              raw[i][e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p.q + at * D) + lane * (E / 2) + e) : 0u;
+              raw[i][e] = r < rows ? load(reinterpret_cast<const uint32_t*>(p.q + at * D) + lane * (E / 2) + e) : 0u;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
