@@ -266,9 +266,15 @@ def make_serve_plan(w: Workload, max_len: int, page: int = 64, e4m3: bool = Fals
 
 def serve_prompt(sp: ServePlan, qkv, o=None, lse=None, stream=None):
     """The prompts' projected rows qkv [B, N, (Hq + 2 Hkv) * d] through the
-    sparse layer; their keys and values fill the cache from position 0.  Returns
-    the attention output [B, Hq, N, d]."""
+    sparse layer; their keys and values fill the cache from position 0.  Every
+    prompt has the plan's N tokens.  Returns the attention output [B, Hq, N, d]."""
     w = sp.plan.w
+    # run_layer hands bare pointers to calls of the plan's own sizes
+    for t, shape, dtype in ((qkv, (w.B, w.N, (w.Hq + 2 * w.Hkv) * w.d), torch.bfloat16),
+                            (o, (w.B, w.Hq, w.N, w.d), torch.bfloat16), (lse, (w.B, w.Hq, w.N), torch.float32)):
+        minf._need(t is None or (t.shape == shape and t.dtype == dtype and t.device == sp.lens.device
+                                 and (t is qkv or t.is_contiguous())),
+                   "serve_prompt (qkv, o and lse of the plan's sizes, types and device)")
     q, k, v = minf.minf_qkv_norm_rope(qkv, w.Hq, w.Hkv, stream=stream, **sp.rotation)
     with torch.cuda.stream(stream):
         if o is None:
