@@ -264,6 +264,14 @@ def make_serve_plan(w: Workload, max_len: int, page: int = 64, e4m3: bool = Fals
     return sp
 
 
+def _on_plan(sp: ServePlan, stream):
+    """The plan's device, and `stream`, one of that device, if given, made current."""
+    if stream is None:
+        return torch.cuda.device(sp.lens.device)
+    minf._need(stream.device == sp.lens.device, "serving call (stream of the plan's device)")
+    return torch.cuda.stream(stream)
+
+
 def serve_prompt(sp: ServePlan, qkv, o=None, lse=None, stream=None):
     """The prompts' projected rows qkv [B, N, (Hq + 2 Hkv) * d] through the
     sparse layer; their keys and values fill the cache from position 0.  Every
@@ -276,7 +284,7 @@ def serve_prompt(sp: ServePlan, qkv, o=None, lse=None, stream=None):
                                  and (t is qkv or t.is_contiguous())),
                    "serve_prompt (qkv, o and lse of the plan's sizes, types and device)")
     q, k, v = minf.minf_qkv_norm_rope(qkv, w.Hq, w.Hkv, stream=stream, **sp.rotation)
-    with torch.cuda.stream(stream):
+    with _on_plan(sp, stream):
         if o is None:
             o = torch.empty_like(q)
         run_layer(sp.plan, q, k, v, o, lse, stream=stream)
@@ -294,7 +302,7 @@ def serve_tokens(sp: ServePlan, qkv, depth=None, tree_mask=None, n_draft=None, s
     :func:`keep_tokens`.  Returns (o [B, Hq, T, d], lse, k, v)."""
     w = sp.plan.w
     B, T, _ = qkv.shape
-    with torch.cuda.stream(stream):
+    with _on_plan(sp, stream):
         if depth is None:
             depth = torch.arange(T, dtype=torch.int32, device=qkv.device)
         pos = sp.lens[:, None] + depth[None]
@@ -309,7 +317,7 @@ def keep_tokens(sp: ServePlan, k, v, count, rows=None, stream=None):
     """Keeps ``count[b]`` tokens of the last step (int32 [B]): the first ones, or
     those of ``rows`` [B, n] in its order (a drafted tree's accepted path, root
     first), whose keys and values move to their final positions."""
-    with torch.cuda.stream(stream):
+    with _on_plan(sp, stream):
         if rows is not None:
             minf.minf_kv_write(k, v, sp.cache, sp.pages, sp.lens, count=count, rows=rows, ws=sp.bufs["ws_cache"])
         sp.lens.add_(count)

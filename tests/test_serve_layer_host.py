@@ -30,3 +30,71 @@ def test_prompt_of_other_sizes_is_refused(sp, kw):
     qkv = torch.zeros(kw.get("B", 2), kw.get("N", 128), kw.get("C", 8 * 64), dtype=kw.get("dtype", torch.bfloat16))
     with pytest.raises(minf.MinfError, match="serve_prompt"):
         layer.serve_prompt(sp, qkv, o=kw.get("o"), lse=kw.get("lse"))
+
+
+# -------------------------------------------- the plan's device, where it is not the current one
+class _Now:
+    """Stands in for torch.cuda's current device and stream, and for the calls; keeps what each call ran on."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.calls = (0, "default"), []
+
+        @contextlib.contextmanager
+        def on(what):
+            was, self.now = self.now, what
+            yield
+            self.now = was
+
+        monkeypatch.setattr(torch.cuda, "device", lambda d: on((torch.device(d).index, "default")))
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: on(self.now if s is None else (s.device.index, s.name)))
+
+        def call(name, result=None):
+            # one with a `stream` argument of its own goes there, or to its tensors' device's current stream
+            def f(*a, stream=None, **kw):
+                self.calls.append((name, self.now if stream is None else (stream.device.index, stream.name)))
+                return result
+            return f
+        t = torch.zeros(2, 2, 4, 64, **BF)
+        monkeypatch.setattr(minf, "minf_qkv_norm_rope", call("rope", (t, t, t)))
+        monkeypatch.setattr(minf, "minf_kv_write", call("write"))
+        monkeypatch.setattr(minf, "minf_tree_attn", call("attn", (t, t)))
+        monkeypatch.setattr(layer, "run_layer", call("layer"))
+
+
+class _Dev1(torch.Tensor):
+    """A host tensor that says it lies on the second GPU."""
+    device = property(lambda self: torch.device("cuda", 1))
+
+
+def _on_dev1(sp):
+    p = types.SimpleNamespace(**vars(sp))
+    p.lens = sp.lens.clone().as_subclass(_Dev1)
+    return p
+
+
+@pytest.mark.parametrize("stream", [None, "side"])
+def test_calls_run_on_the_plans_device(sp, monkeypatch, stream):
+    """The current device is 0, the plan lies on device 1: every call of a step, and run_layer's bare pointers above
+    all, is made with device 1 current, on its default stream or on the given one."""
+    now = _Now(monkeypatch)
+    p = _on_dev1(sp)
+    st = types.SimpleNamespace(device=torch.device("cuda", 1), name="side") if stream else None
+    monkeypatch.setattr(torch, "arange", lambda *a, **kw: torch.tensor([0, 1, 2, 3], dtype=torch.int32))
+    layer.serve_prompt(p, torch.zeros(2, 128, 8 * 64, **BF).as_subclass(_Dev1), stream=st)
+    layer.serve_tokens(p, torch.zeros(2, 4, 8 * 64, **BF).as_subclass(_Dev1), stream=st)
+    layer.keep_tokens(p, torch.zeros(2, 2, 4, 64, **BF), torch.zeros(2, 2, 4, 64, **BF), torch.ones(2, dtype=torch.int32),
+                      rows=torch.zeros(2, 3, dtype=torch.int32), stream=st)
+    assert {n for n, _ in now.calls} == {"rope", "write", "attn", "layer"}
+    assert [c for c in now.calls[1:] if c[1] != (1, stream or "default")] == []
+    assert now.calls[0][0] == "rope" and now.now == (0, "default")
+
+
+def test_stream_of_another_device_is_refused(sp, monkeypatch):
+    now = _Now(monkeypatch)
+    p = _on_dev1(sp)
+    st = types.SimpleNamespace(device=torch.device("cuda", 0), name="side")
+    x = torch.zeros(2, 4, 8 * 64, **BF).as_subclass(_Dev1)
+    for call in (lambda: layer.serve_tokens(p, x, stream=st), lambda: layer.keep_tokens(p, x, x, torch.ones(2), stream=st)):
+        with pytest.raises(minf.MinfError, match="stream"):
+            call()
+    assert now.calls == []
