@@ -98,3 +98,32 @@ def test_stream_of_another_device_is_refused(sp, monkeypatch):
         with pytest.raises(minf.MinfError, match="stream"):
             call()
     assert now.calls == []
+
+
+# ------------------------------------------------------------------ what keep_tokens keeps
+@pytest.mark.parametrize("with_rows", [False, True])
+@pytest.mark.parametrize("count,n_draft,kept", [
+    ([0, 4], None, [0, 4]), ([5, 2], None, [4, 2]), ([-1, 1 << 30], None, [0, 4]), ([-2147483648, 2147483647], None, [0, 4]),
+    ([3, 3], [2, 4], [2, 3]), ([4, -1], [0, 0], [0, 0]), ([4, 4], [-2, 9], [0, 4])])
+def test_kept_counts_are_bounded(sp, monkeypatch, with_rows, count, n_draft, kept):
+    """The cached lengths move by no more than the step's tokens, and what is moved in the cache goes with them."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    wrote = []
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(minf, "minf_kv_write", lambda *a, count=None, **kw: wrote.append(count.tolist()))
+    p = types.SimpleNamespace(**vars(sp))
+    p.lens = i32([130, 100])
+    k = torch.zeros(2, 2, 4, 64, **BF)
+    rows = torch.zeros(2, 4, dtype=torch.int32) if with_rows else None
+    layer.keep_tokens(p, k, k, i32(count), rows=rows, n_draft=None if n_draft is None else i32(n_draft))
+    assert p.lens.tolist() == [130 + kept[0], 100 + kept[1]] and p.lens.dtype == torch.int32
+    assert wrote == ([kept] if with_rows else [])
+
+
+def test_kept_tokens_stay_within_the_pages(sp, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    p = types.SimpleNamespace(**vars(sp))                        # 160 positions a sequence
+    p.lens = torch.tensor([158, 160], dtype=torch.int32)
+    for _ in range(3):
+        layer.keep_tokens(p, None, None, torch.tensor([2, 1], dtype=torch.int32))
+    assert p.lens.tolist() == [160, 160]
