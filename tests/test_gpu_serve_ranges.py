@@ -142,3 +142,82 @@ def test_one_channel_row_beside_far_scores(rows, nats, where, size, e4m3):
         v[where, 5] = size
     floor = (2.0 ** -29 if rows <= 64 else 2.0 ** -27) if e4m3 else 0.0
     check(*one_block(rows, 128 if nats != 14 else 64, e4m3, nats, where, channel), floor=floor)
+
+
+def small_cache(e4m3, L, d=128, page=32, seed=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = -(-L // page)
+    c = minf.KVCache.empty(n, 2, page, d, e4m3)
+    pages = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    k, v = (torch.randn(1, 2, L, d, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv")
+    return c, pages, k, v, g
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,Hq", [(3, 4), (10, 4), (20, 4), (40, 8)])
+def test_non_finite_rows_reach_who_sees_them(T, Hq, e4m3):
+    """A NaN key or value of the context makes every row of its KV head NaN (with 16-bit values, in its channel
+    only); a NaN key of a drafted token makes the rows NaN that see it, and no other row changes."""
+    ctx, d, G = 300, 128, Hq // 2
+    c, pages, k, v, g = small_cache(e4m3, ctx + T)
+    q = torch.randn(1, Hq, T, d, generator=g, device="cuda").to(torch.bfloat16)
+    see = torch.rand(T, T, generator=g, device="cuda") < 0.5
+    see[:, 1] = torch.arange(T, device="cuda") % 2 == 0           # who sees drafted token 1
+    mask = (see.long() << torch.arange(T, device="cuda")).sum(-1)[None].contiguous()
+    ws = minf.tree_attn_workspace(1, Hq, 2, T, d)
+    zero, lens = torch.zeros(1, **I32), torch.full((1,), ctx, **I32)
+
+    def attend(k, v):
+        minf.minf_kv_write(k, v, c, pages, zero, ws=ws)
+        r = minf.minf_tree_attn(q, c, pages, lens, tree_mask=mask, ws=ws)
+        assert minf.minf_get_device_status(ws) == 0
+        return r
+
+    o, lse = attend(k, v)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    bad = k.clone()
+    bad[0, 0, 7, 3] = math.nan
+    o1, l1 = attend(bad, v)
+    assert torch.isnan(o1[0, :G]).all() and torch.isnan(l1[0, :G]).all()
+    assert torch.equal(o1[0, G:], o[0, G:]) and torch.equal(l1[0, G:], lse[0, G:])
+    bad = v.clone()
+    bad[0, 1, 150, 9] = math.nan
+    o1, l1 = attend(k, bad)
+    nan = torch.isnan(o1[0, G:])
+    assert nan.all() if e4m3 else (nan[..., 9].all() and nan.sum() == nan[..., 9].numel())
+    assert torch.equal(o1[0, :G], o[0, :G]) and torch.equal(l1[0, :G], lse[0, :G])
+    bad = k.clone()
+    bad[0, 0, ctx + 1] = math.nan
+    o1, l1 = attend(bad, v)
+    sees = see[:, 1]
+    assert torch.isnan(o1[0, :G, sees]).all() and torch.isnan(l1[0, :G, sees]).all()
+    assert torch.equal(o1[0, :G, ~sees], o[0, :G, ~sees]) and torch.equal(l1[0, :G, ~sees], lse[0, :G, ~sees])
+    assert torch.equal(o1[0, G:], o[0, G:])
+
+
+def test_eager_calls_beside_a_replayed_graph():
+    """The same cache, read by a replayed graph and by eager calls on another stream, each with a workspace of its
+    own: both sides give what they give alone."""
+    c, pages, k, v, g = small_cache(True, 3000)
+    lens = torch.tensor([2990], **I32)
+    minf.minf_kv_write(k, v, c, pages, torch.zeros(1, **I32))
+    qs = [torch.randn(1, 8, T, 128, generator=g, device="cuda").to(torch.bfloat16) for T in (1, 6)]
+    ws = [minf.tree_attn_workspace(1, 8, 2, 6, 128) for _ in qs]
+    alone = [minf.minf_tree_attn(q, c, pages, lens, ws=w) for q, w in zip(qs, ws)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = minf.minf_tree_attn(qs[0], c, pages, lens, ws=ws[0])
+    torch.cuda.synchronize()
+    eager, replayed = [], []
+    for _ in range(30):
+        with torch.cuda.stream(side):
+            graph.replay()
+            replayed.append(tuple(t.clone() for t in got))
+        eager.append(minf.minf_tree_attn(qs[1], c, pages, lens, ws=ws[1]))
+    torch.cuda.synchronize()
+    for outs, want, w in ((replayed, alone[0], ws[0]), (eager, alone[1], ws[1])):
+        assert minf.minf_get_device_status(w) == 0
+        for o, lse in outs:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
