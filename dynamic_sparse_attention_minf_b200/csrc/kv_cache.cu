@@ -84,9 +84,10 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& q, uint32_t exp_byte) 
 
 // One row of K and one of V per group of D / 8 lanes, kUnroll of them in
 // flight; a block takes kRows * kUnroll tokens of one head.  Bound by memory:
-// a 131,072-token prompt of 8 heads of 128 in 8 bits moves 807 MB in 137 us,
-// 0.90 of the measured copy rate; back (kv_read_kernel) in 130 us, 0.95.
-// (Two rows in flight: 139 us, eight: 159 us.)
+// a 131,072-token prompt of 8 heads of 128 in 8 bits moves 807 MB in 136 us in a
+// row of calls, 0.90 of the measured copy rate; back (kv_read_kernel) in 131 us,
+// 0.94; in 16 bits 1,074 MB in 166 and 165 us, 0.98 and 0.99.  (Two rows in flight:
+// 139 us, eight: 159 us.)
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p, int chunks) {
   constexpr int L = D / 8;

@@ -30,10 +30,10 @@ __device__ __forceinline__ float2 halves(uint32_t two) {  // of a bf16 pair
 // and sines of their own eight elements once, for all of those heads.
 //
 // Bound by memory (each row is read and written once: 131,072 tokens of 48 heads
-// of 128 take 567 us, 0.87 of the measured copy rate; fewer or more rows in
-// flight, more threads or streaming accesses take 572 to 670) as long as few
-// instructions go with a row: with the weights multiplied into the cosines and
-// sines of the query and then the key heads,
+// of 128 take 521 us in a row of calls, 0.94 of the measured copy rate; through
+// read-only loads 549, and with those fewer or more rows in flight, more threads or
+// streaming accesses up to 670) as long as few instructions go with a row: with the
+// weights multiplied into the cosines and sines of the query and then the key heads,
 //   y = inv * (x * (c w) + partner * (s w')),  inv = rsqrt(mean(x^2) + eps),
 // and the partner arrives by exchanging the rows as read, two elements a word.
 template <int D>

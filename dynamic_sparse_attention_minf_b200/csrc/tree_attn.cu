@@ -9,9 +9,10 @@
 //
 // What bounds it is reading the cache once: a KV head's T * (Hq / Hkv) rows share
 // each key, so there are few operations per byte, and everything here serves to
-// keep loads in flight.  8 KV heads of 128: one token over 262,144 positions takes
-// 98 us in 8 bits (5.5 TB/s of the measured 6.55) and 170 us in 16 (6.3 TB/s), 64
-// rows over 131,072 in 16 bits 94 us; the smallest calls 9 to 11 us, one-off steps.
+// keep loads in flight.  8 KV heads of 128, calls in a row at full clocks: one token
+// over 262,144 positions takes 99 us in 8 bits (5.5 TB/s of the measured 6.55) and
+// 171 us in 16 (6.3 TB/s), 64 rows over 131,072 in 16 bits 94 us and in 8 bits 108;
+// the smallest calls 9 to 11 us, one-off steps.
 //  * The products run transposed on the tensor cores, S^T = K Q^T and O^T =
 //    V^T P: the 128 keys of a tile (then the d elements of a value) are the 128
 //    rows of the instruction, and the query rows are its N = 16 .. 64 columns,

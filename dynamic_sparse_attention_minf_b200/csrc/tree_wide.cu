@@ -8,9 +8,12 @@
 //
 // Bound, for 16-bit caches, by the softmax's chain and the tensor pipe (1024
 // cycles a tile) rather than by memory: 256 rows of each of 8 KV heads over 131,064
-// positions take 143 us (208 transposed), 225 us in 8 bits (357 transposed).  8-bit keys, values, queries and weights
-// are multiplied as tree_attn.cu describes; the keys' and values' powers of two
-// are read per tile from shared memory, a row's own factor from its thread.
+// positions take 142 to 147 us at full clocks (208 transposed; 168 to 180 in long
+// rows of calls, under the power cap), 225 us in 8 bits (357 transposed).  8-bit keys,
+// values, queries and weights are multiplied as tree_attn.cu describes; the keys' and
+// values' powers of two are read per tile from shared memory, a row's own factor from
+// its thread.  All exponentials are the hardware's: running part of them as
+// polynomials on the FMA pipe, as the pre-fill kernel does, has not been measured.
 #include <cuda_fp8.h>
 
 #include <type_traits>

@@ -334,7 +334,7 @@ def keep_tokens(sp: ServePlan, k, v, count, rows=None, stream=None, n_draft=None
 
 def cached_prefix(sp: ServePlan, N: int, stream=None):
     """Dense K, V [B, Hkv, N, d] of the cached positions (zeros behind a
-    sequence's last), as the pre-fill calls read them."""
+    sequence's last), as the pre-fill calls read them; those take N queries too."""
     return minf.minf_kv_read(sp.cache, sp.pages, sp.lens, N, ws=sp.bufs["ws_cache"], stream=stream)
 
 

@@ -453,7 +453,8 @@ def minf_selftest_exp2(x, stream=None):
 # built from binding.cpp.  Mismatched tensors (type, shape, device, contiguity)
 # raise MinfError with "invalid argument".  A call runs on its tensors' device,
 # on that device's current stream unless `stream` says otherwise, and allocates
-# missing outputs there.
+# missing outputs there.  Without `ws` a call makes a zeroed one, and what it
+# reports there (bad ids or lengths) is not seen.
 E4M3 = torch.float8_e4m3fn
 _ext = None
 

@@ -402,8 +402,10 @@ minf_status minf_attn_grid(const minf_shape* shape, const minf_bf16* Q, const mi
  * Serving: what stands right before and right after pre-fill.  The projected
  * rows of a layer become the Q, K and V that the calls above read; K and V go
  * into a paged cache; new tokens (one, or a tree of drafted ones) attend over
- * it; and a cached prefix comes back as dense K and V for the pre-fill of what
- * follows it.  MInference covers pre-fill only and has no counterpart.
+ * it; and a cached prefix comes back as dense K and V.  (The pre-fill calls take
+ * as many queries as keys, so one that starts from a cached prefix needs the
+ * prefix's queries too; up to 64 new rows at a time need minf_tree_attn alone.)
+ * MInference covers pre-fill only and has no counterpart.
  *
  * These calls take any number of rows, not only multiples of 128.  Those that
  * read device-resident ids or lengths take a workspace `ws`, zeroed once, whose
