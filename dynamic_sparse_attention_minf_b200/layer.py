@@ -317,13 +317,11 @@ def keep_tokens(sp: ServePlan, k, v, count, rows=None, stream=None, n_draft=None
     """Keeps ``count[b]`` tokens of the last step (int32 [B]): the first ones, or
     those of ``rows`` [B, n] in its order (a drafted tree's accepted path, root
     first), whose keys and values move to their final positions.  A count below 0
-    or above what the step brought (``n_draft[b]``, if given, of k's tokens) or
-    what ``rows`` names counts as the nearest that is not, and no sequence grows
-    beyond its pages."""
+    or above the tokens that there are (``n_draft[b]``, if given; those that
+    ``rows`` names, or k's) counts as the nearest that is not, and no sequence
+    grows beyond its pages."""
     with _on_plan(sp, stream):
-        most = None if k is None else k.size(2)
-        if rows is not None:
-            most = rows.size(1) if most is None else min(most, rows.size(1))
+        most = rows.size(1) if rows is not None else None if k is None else k.size(2)
         if n_draft is not None:
             count = torch.minimum(count, n_draft)
         count = torch.clamp(count, 0, most)

@@ -447,7 +447,9 @@ enum { MINF_KV_BF16 = 0, MINF_KV_E4M3 = 1 };
  * A paged key-value cache, caller-owned device memory (16-byte aligned):
  *   k, v   [n_pages, Hkv, page, d] bf16, or e4m3 bytes
  *   k_exp, v_exp [n_pages, Hkv, page] (e4m3 only): a row's values are its bytes'
- *          times 2^(exp - 127); 255 marks a row that held a NaN or an infinity
+ *          times 2^(exp - 127); 255 marks a row that held a NaN or an infinity.
+ *          minf_kv_write stores 47 to 247, and minf_tree_attn takes a value row's
+ *          smaller one as 47 (a pool of zero bytes holds rows of zeros)
  * page in {16, 32, 64, 128}, d in {64, 128}, n_pages * Hkv * page < 2^31.
  * A batch's page table `pages` [B, max_pages] says where its sequences lie:
  * position j of sequence b is row j % page of page pages[b, j / page].  Entries
