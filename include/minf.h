@@ -511,7 +511,7 @@ size_t minf_tree_attn_workspace(int B, int Hq, int Hkv, int T, int d);
  * largest, and are off by up to 2^-17 of it below that.  The weights, times
  * their value row's power of two, keep 9 bits down to 2^-18 of the row's largest
  * such product, and are off by up to 2^-27 of it below that; value rows of zeros
- * do not count in it.  (So a key far above the others hides them in no channel
+ * count in it with 2^-80.  (So a key far above the others hides them in no channel
  * where they weigh more than that, even where its own values are zero.)
  */
 minf_status minf_tree_attn(const minf_kv_cache* cache, const minf_bf16* Q, int B, int Hq, int T, float scale,
